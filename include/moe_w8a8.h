@@ -613,6 +613,188 @@ moe_status moe_w8a8_ep_combine_blocked(const moe_w8a8_weights* w, const float* o
                                        const int32_t* rank_first, int32_t world, int32_t block_tokens, void* y,
                                        const void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the layer: the other operators of a W8A8 model's serving step.
+ *
+ * Dense products (attention projections, the LM head; "MiniMax-M3 W8A8 on
+ * K100AI", s1.2 and s3.2, the expert products' rules without the experts):
+ *   quant:  v = x[t][j] inv_s[j] (or x[t][j] without smoothing), sx[t] =
+ *           max_j |v| / 127, xq = rint(v / sx) clamped to +-127;
+ *   y[t][n] = (sum_j xq[t][j] wq[n][j]) sx[t] sw[n] + bias[n],
+ * the sum exact in INT32, then one fp32 rounding per operation and one to the
+ * output type.  A token that holds an infinity or a NaN gets NaN outputs.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+    int32_t n;             /* output channels, 1 .. MOE_LINEAR_MAX_N                           */
+    int32_t k;             /* inputs, 1 .. MOE_LINEAR_MAX_K                                    */
+    float alpha;           /* SmoothQuant migration strength in [0, 1] (moe_w8a8_linear_prepare) */
+    int32_t in_dtype;      /* MOE_F32 or MOE_BF16: x                                           */
+    int32_t out_dtype;     /* MOE_F32 or MOE_BF16: y                                           */
+} moe_w8a8_linear_config;
+
+#define MOE_LINEAR_MAX_N (1 << 20)
+#define MOE_LINEAR_MAX_K 16384
+
+typedef struct moe_w8a8_linear moe_w8a8_linear; /* opaque, library-owned */
+
+/*
+ * Quantise the weights of a product, per output channel.
+ *   w           device fp32 [k][n]  (y = x w)
+ *   bias        device fp32 [n], or NULL
+ *   act_absmax  device fp32 [k] (moe_w8a8_calibrate_absmax): s_j = max|X_j|^alpha /
+ *               max|W_j|^(1-alpha) is folded into the weights; NULL: no smoothing
+ * Synchronises `stream`; the inputs may be freed afterwards.  Allocates the
+ * handle's device memory (n k bytes, padded to multiples of 256 channels and
+ * 128 inputs, and scales); MOE_ERR_OOM if that fails.
+ */
+moe_status moe_w8a8_linear_prepare(const moe_w8a8_linear_config* cfg, const float* w, const float* bias,
+                                   const float* act_absmax, moe_stream_t stream, moe_w8a8_linear** out);
+
+/*
+ * The same from weights that are codes already (a quantised checkpoint).
+ *   wq     device INT8 [n][k];  sw  device fp32 [n];  bias  device fp32 [n] or NULL
+ *   inv_s  device fp32 [k], what x is multiplied with before it is quantised, or NULL
+ */
+moe_status moe_w8a8_linear_prepare_codes(const moe_w8a8_linear_config* cfg, const int8_t* wq, const float* sw,
+                                         const float* bias, const float* inv_s, moe_stream_t stream,
+                                         moe_w8a8_linear** out);
+
+/* Bytes of device workspace moe_w8a8_linear_forward needs for up to
+ * max_tokens tokens (0 on a NULL handle or negative max_tokens). */
+size_t moe_w8a8_linear_workspace_size(const moe_w8a8_linear* l, int32_t max_tokens);
+
+/*
+ * y = dequant(quant(x) wq^T) + bias for T tokens (T = 0 is a no-op).
+ *   x  device [T][k], cfg.in_dtype, rows ldx elements apart (ldx >= k)
+ *   y  device [T][n], cfg.out_dtype, rows ldy elements apart (ldy >= n); what
+ *      lies between the rows and after the last one is left as it was
+ *   workspace  device, >= moe_w8a8_linear_workspace_size(l, T), 256-byte aligned
+ * x and y need the alignment of their type only; rows on 16-byte boundaries
+ * are read and written with wider accesses.  Calls that share a workspace must
+ * not overlap on the device.  The handle's device must be current.
+ */
+moe_status moe_w8a8_linear_forward(const moe_w8a8_linear* l, const void* x, int64_t ldx, int32_t T, void* y, int64_t ldy,
+                                   void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/*
+ * The product alone, from codes that a producer has formed (moe_w8a8_block_norm).
+ *   xq  device INT8 [T][k], 16-byte aligned, rows ldq bytes apart (ldq >= k, a
+ *       multiple of 16; what follows the k codes of a row is not used)
+ *   sx  device fp32 [T]
+ */
+moe_status moe_w8a8_linear_forward_codes(const moe_w8a8_linear* l, const int8_t* xq, int64_t ldq, const float* sx,
+                                         int32_t T, void* y, int64_t ldy, moe_stream_t stream);
+
+/* Copy the prepared weights out (device pointers, each may be NULL): wq INT8
+ * [n][k], sw fp32 [n], inv_s fp32 [k] (MOE_ERR_INVALID_ARG without smoothing). */
+moe_status moe_w8a8_linear_export(const moe_w8a8_linear* l, int8_t* wq, float* sw, float* inv_s, moe_stream_t stream);
+
+/* Synchronise `stream` and read (and clear) the handle's status word: MOE_OK,
+ * or MOE_ERR_TIMEOUT when a bounded wait in a kernel ran out since the last check. */
+moe_status moe_w8a8_linear_check_status(const moe_w8a8_linear* l, moe_stream_t stream);
+
+/* Free the handle (NULL is a no-op); no enqueued forward may still use it. */
+void moe_w8a8_linear_destroy(moe_w8a8_linear* l);
+
+/* ---------------------------------------------------------------------------
+ * The norms around a block, in one pass: with rms(v) = sqrt(mean v^2 + eps),
+ *   p = b, or b / rms(b) * (w_post + weight_offset)     the norm after the block
+ *   r = residual_scale x + branch_scale g p             the new residual stream
+ *   n = r / rms(r) * (w_pre + weight_offset)            the norm before the next block
+ * r is rounded to the stream's type before its own norm.  Codes of n for the
+ * next product: v = r (w_pre + weight_offset) inv_s, s = max|v| / 127, xq =
+ * rint(v / s), sx = s / rms(r) (the row's rms cancels in v / s).  Without
+ * w_pre the codes are those of r, the layer's own quantisation of a token.
+ * The gate g is 1, a value per channel, per token or per element, or its
+ * sigmoid.  Sums of squares are held in fp32: |values| up to 1e18.
+ * ------------------------------------------------------------------------ */
+
+enum {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_CHANNEL = 1,  /* gate: fp32 [d]                              */
+    MOE_GATE_TOKEN = 2,    /* gate: fp32 [T]                              */
+    MOE_GATE_ELEMENT = 3   /* gate: in_dtype [T][d], rows ldg apart       */
+};
+
+typedef struct {
+    int32_t d;             /* 1 .. MOE_NORM_MAX_D                                  */
+    int32_t in_dtype;      /* MOE_F32 or MOE_BF16: b (and an element gate)         */
+    int32_t res_dtype;     /* MOE_F32 or MOE_BF16: x, x_out                        */
+    int32_t out_dtype;     /* MOE_F32 or MOE_BF16: n_out                           */
+    int32_t gate;          /* MOE_GATE_*                                           */
+    int32_t gate_sigmoid;  /* 1: the gate passes through a sigmoid                 */
+    float eps;             /* > 0                                                  */
+    float residual_scale, branch_scale;
+    float weight_offset;   /* added to both norms' weights (1 for weights around 0) */
+} moe_w8a8_norm_config;
+
+#define MOE_NORM_MAX_D 16384
+
+/* Device pointers; ld*: elements between rows, >= d. */
+typedef struct {
+    const void* b;         /* [T][d] block output, or NULL (then x is needed, and no gate or w_post) */
+    int64_t ldb;
+    const void* x;         /* [T][d] residual stream, or NULL: zeros                       */
+    int64_t ldx;
+    const void* gate;      /* by cfg.gate; NULL for MOE_GATE_NONE                          */
+    int64_t ldg;
+    const float* w_post;   /* [d], or NULL: no norm after the block                        */
+    const float* w_pre;    /* [d], or NULL: no norm before the next block (no n_out)       */
+    const float* inv_s;    /* [d] smoothing of the codes, or NULL                          */
+    void* x_out;           /* [T][d] r, or NULL; may be x itself                           */
+    int64_t ldxo;
+    void* n_out;           /* [T][d] n, or NULL; may be b itself when the types are equal   */
+    int64_t ldn;
+    int8_t* xq;            /* [T][d] codes, or NULL; 16-byte aligned                       */
+    int64_t ldq;           /* a multiple of 16                                             */
+    float* sx;             /* [T], with xq                                                 */
+} moe_w8a8_norm_io;
+
+/* T rows (T = 0 is a no-op).  At least one of x_out, n_out and xq is given.
+ * A row that holds an infinity or a NaN gets codes 0 and the scale NaN. */
+moe_status moe_w8a8_block_norm(const moe_w8a8_norm_config* cfg, const moe_w8a8_norm_io* io, int32_t T, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The next token of each row of logits, from given random numbers.  In order:
+ *   1. a token takes part if its `allowed` bit is set and its logit is neither
+ *      -infinity nor NaN; what stands in the place of one that may not be
+ *      chosen does not matter.  A row with none gives token -1, prob 0.
+ *   2. the tokens by falling logit, the lowest index first on ties; the first
+ *      top_k of them.
+ *   3. with masses e_i = exp((l_i - max l) / temperature): the shortest prefix
+ *      whose mass reaches top_p of the whole, one token at least.
+ *   4. of those the ones with e_i >= min_p.
+ *   5. in the order of the tokens, the first whose running mass exceeds
+ *      u times the mass that is left.
+ * Logits of +infinity share the mass evenly.  Results do not depend on the
+ * order of execution; masses are held as integers of 2^-45 of the largest one,
+ * one unit at least (below 2^-1000 of the largest: none).
+ * ------------------------------------------------------------------------ */
+
+/* Device pointers. */
+typedef struct {
+    const void* logits;        /* [rows][vocab] fp32 or bf16, rows ld elements apart              */
+    int64_t ld;
+    const int32_t* allowed;    /* [rows][ceil(vocab / 32)] words, bit i of word j: token 32 j + i;
+                                  rows ld_allowed words apart.  NULL: every token                */
+    int64_t ld_allowed;
+    const float* temperature;  /* [rows]; not above 0: the largest logit (lowest index), prob 1.
+                                  NULL: 1                                                        */
+    const int32_t* top_k;      /* [rows]; not above 0: off.  NULL: off                           */
+    const float* top_p;        /* [rows]; not below 1: off.  NULL: off                           */
+    const float* min_p;        /* [rows]; not above 0: off, above 1 counts as 1.  NULL: off       */
+    const float* u;            /* [rows] in [0, 1)                                               */
+    int32_t* token;            /* [rows]                                                         */
+    float* prob;               /* [rows] the token's share of the mass that is left, or NULL     */
+} moe_w8a8_sample_io;
+
+#define MOE_SAMPLE_MAX_VOCAB (1 << 18)
+#define MOE_SAMPLE_MAX_ROWS (1 << 20)
+
+/* dtype: MOE_F32 or MOE_BF16 (logits).  rows = 0 is a no-op. */
+moe_status moe_w8a8_sample(const moe_w8a8_sample_io* io, int32_t rows, int32_t vocab, int32_t dtype, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,12 +48,26 @@ EXPORTS = (
     "moe_w8a8_set_fused_threshold", "moe_w8a8_set_cta_pairs",
     "moe_w8a8_ep_block_rows", "moe_w8a8_ep_pack", "moe_w8a8_ep_experts_blocked_workspace_size",
     "moe_w8a8_ep_experts_blocked", "moe_w8a8_ep_combine_blocked",
+    "moe_w8a8_linear_prepare", "moe_w8a8_linear_prepare_codes", "moe_w8a8_linear_workspace_size",
+    "moe_w8a8_linear_forward", "moe_w8a8_linear_forward_codes", "moe_w8a8_linear_export",
+    "moe_w8a8_linear_check_status", "moe_w8a8_linear_destroy", "moe_w8a8_block_norm", "moe_w8a8_sample",
 )
 
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 MOE_PEAK_MAX_MMA = 1 << 24
 
 MOE_N_STAGES = 8
+
+MOE_LINEAR_MAX_N = 1 << 20
+MOE_LINEAR_MAX_K = 16384
+MOE_NORM_MAX_D = 16384
+MOE_SAMPLE_MAX_VOCAB = 1 << 18
+MOE_SAMPLE_MAX_ROWS = 1 << 20
+
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+MOE_GATE_ELEMENT = 3
 
 
 class MoeError(RuntimeError):
@@ -76,6 +90,33 @@ _DBG_FIELDS = ("logits", "topk_idx", "topk_w", "offsets", "row2ts", "ts2row", "x
 
 class moe_w8a8_debug(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _DBG_FIELDS]
+
+
+class moe_w8a8_linear_config(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("k", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class moe_w8a8_norm_config(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("gate", ctypes.c_int32), ("gate_sigmoid", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class moe_w8a8_norm_io(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_void_p), ("ldb", ctypes.c_int64), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64),
+                ("gate", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("w_post", ctypes.c_void_p),
+                ("w_pre", ctypes.c_void_p), ("inv_s", ctypes.c_void_p), ("x_out", ctypes.c_void_p),
+                ("ldxo", ctypes.c_int64), ("n_out", ctypes.c_void_p), ("ldn", ctypes.c_int64),
+                ("xq", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("sx", ctypes.c_void_p)]
+
+
+class moe_w8a8_sample_io(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("allowed", ctypes.c_void_p),
+                ("ld_allowed", ctypes.c_int64), ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p), ("u", ctypes.c_void_p),
+                ("token", ctypes.c_void_p), ("prob", ctypes.c_void_p)]
 
 
 _lib = None
@@ -132,6 +173,19 @@ def lib():
             "moe_w8a8_ep_experts_blocked_workspace_size": ([vp, i32, i32], sz),
             "moe_w8a8_ep_experts_blocked": ([vp, vp, i32, i32, vp, vp, sz, vp, vp], i32),
             "moe_w8a8_ep_combine_blocked": ([vp, vp, i32, vp, i32, i32, vp, vp, sz, vp], i32),
+            "moe_w8a8_linear_prepare": ([ctypes.POINTER(moe_w8a8_linear_config), vp, vp, vp, vp,
+                                         ctypes.POINTER(vp)], i32),
+            "moe_w8a8_linear_prepare_codes": ([ctypes.POINTER(moe_w8a8_linear_config), vp, vp, vp, vp, vp,
+                                               ctypes.POINTER(vp)], i32),
+            "moe_w8a8_linear_workspace_size": ([vp, i32], sz),
+            "moe_w8a8_linear_forward": ([vp, vp, i64, i32, vp, i64, vp, sz, vp], i32),
+            "moe_w8a8_linear_forward_codes": ([vp, vp, i64, vp, i32, vp, i64, vp], i32),
+            "moe_w8a8_linear_export": ([vp, vp, vp, vp, vp], i32),
+            "moe_w8a8_linear_check_status": ([vp, vp], i32),
+            "moe_w8a8_linear_destroy": ([vp], None),
+            "moe_w8a8_block_norm": ([ctypes.POINTER(moe_w8a8_norm_config), ctypes.POINTER(moe_w8a8_norm_io), i32, vp],
+                                    i32),
+            "moe_w8a8_sample": ([ctypes.POINTER(moe_w8a8_sample_io), i32, i32, i32, vp], i32),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -575,6 +629,185 @@ def moe_w8a8_ep_combine_blocked(w: Weights, o_blocks, T: int, rank_first, block_
         w.handle, _dev_ptr(o_blocks, torch.float32, "o_blocks"), int(T), ptr, int(world), int(block_tokens),
         _dev_ptr(y, _act_dtype(w.cfg.out_dtype), "y"), _dev_ptr(workspace, name="workspace"), _nbytes(workspace),
         _stream(stream)), "moe_w8a8_ep_combine_blocked")
+
+
+# ------------------------------------------------------------------ around the layer
+
+def _cuda(t, name, dtypes, dev):
+    """A CUDA tensor of one of the types on the current device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
+
+
+def _matrix(t, rows, cols, name, dtypes, dev):
+    """Pointer and row stride of a [>= rows][>= cols] tensor whose rows are contiguous."""
+    _cuda(t, name, dtypes, dev)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < rows or shape[1] < cols:
+        raise ValueError(f"{name} must be at least [{rows}][{cols}], got {list(shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:
+        ld = max(ld, cols + -cols % 16)   # the stride of a single row is not used; a round one keeps wide accesses
+    elif ld < cols:
+        raise ValueError(f"{name} has rows {ld} apart that hold {cols} values")
+    return t.data_ptr(), ld
+
+
+def _vector(t, n, name, dtypes, dev):
+    """Pointer of a contiguous tensor of at least n values; None stays None."""
+    if t is None:
+        return None
+    _cuda(t, name, dtypes, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, the call reads or writes {n}")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    return _torch().cuda.current_device()
+
+
+def _types(code: int):
+    return (_act_dtype(code),)
+
+
+def _f32():
+    return (_torch().float32,)
+
+
+class Linear:
+    """Owner of a prepared dense product (destroyed with the object)."""
+
+    def __init__(self, handle: ctypes.c_void_p, cfg: moe_w8a8_linear_config, smooth: bool):
+        self.handle = handle
+        self.cfg = cfg
+        self.smooth = smooth
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.moe_w8a8_linear_destroy(self.handle)
+            self.handle = None
+
+
+def make_linear_config(n, k, alpha=0.6, in_dtype=MOE_BF16, out_dtype=MOE_BF16) -> moe_w8a8_linear_config:
+    return moe_w8a8_linear_config(n, k, alpha, in_dtype, out_dtype)
+
+
+def moe_w8a8_linear_prepare(cfg: moe_w8a8_linear_config, w, bias=None, act_absmax=None, stream=None) -> Linear:
+    dev, f32 = _device(), _f32()
+    h = ctypes.c_void_p()
+    _check(lib().moe_w8a8_linear_prepare(
+        ctypes.byref(cfg), _vector(w, cfg.k * cfg.n, "w", f32, dev), _vector(bias, cfg.n, "bias", f32, dev),
+        _vector(act_absmax, cfg.k, "act_absmax", f32, dev), _stream(stream), ctypes.byref(h)),
+        "moe_w8a8_linear_prepare")
+    return Linear(h, cfg, act_absmax is not None)
+
+
+def moe_w8a8_linear_prepare_codes(cfg: moe_w8a8_linear_config, wq, sw, bias=None, inv_s=None, stream=None) -> Linear:
+    dev, f32 = _device(), _f32()
+    h = ctypes.c_void_p()
+    _check(lib().moe_w8a8_linear_prepare_codes(
+        ctypes.byref(cfg), _vector(wq, cfg.n * cfg.k, "wq", (_torch().int8,), dev), _vector(sw, cfg.n, "sw", f32, dev),
+        _vector(bias, cfg.n, "bias", f32, dev), _vector(inv_s, cfg.k, "inv_s", f32, dev), _stream(stream),
+        ctypes.byref(h)), "moe_w8a8_linear_prepare_codes")
+    return Linear(h, cfg, inv_s is not None)
+
+
+def moe_w8a8_linear_workspace_size(l: Linear, max_tokens: int) -> int:
+    return int(lib().moe_w8a8_linear_workspace_size(l.handle, int(max_tokens)))
+
+
+def moe_w8a8_linear_forward(l: Linear, x, T: int, y, workspace, stream=None):
+    c, dev = l.cfg, _device()
+    if T == 0:
+        return
+    xp, ldx = _matrix(x, T, c.k, "x", _types(c.in_dtype), dev)
+    yp, ldy = _matrix(y, T, c.n, "y", _types(c.out_dtype), dev)
+    _check(lib().moe_w8a8_linear_forward(l.handle, xp, ldx, T, yp, ldy, _vector(workspace, 0, "workspace",
+                                                                                (workspace.dtype,), dev),
+                                         _nbytes(workspace), _stream(stream)), "moe_w8a8_linear_forward")
+
+
+def moe_w8a8_linear_forward_codes(l: Linear, xq, sx, T: int, y, stream=None):
+    c, dev = l.cfg, _device()
+    if T == 0:
+        return
+    qp, ldq = _matrix(xq, T, c.k, "xq", (_torch().int8,), dev)
+    yp, ldy = _matrix(y, T, c.n, "y", _types(c.out_dtype), dev)
+    _check(lib().moe_w8a8_linear_forward_codes(l.handle, qp, ldq, _vector(sx, T, "sx", _f32(), dev), T, yp, ldy,
+                                               _stream(stream)), "moe_w8a8_linear_forward_codes")
+
+
+def moe_w8a8_linear_export(l: Linear, stream=None) -> dict:
+    torch = _torch()
+    c, dev = l.cfg, torch.device("cuda", _device())
+    out = dict(wq=torch.empty((c.n, c.k), dtype=torch.int8, device=dev),
+               sw=torch.empty(c.n, dtype=torch.float32, device=dev),
+               inv_s=torch.empty(c.k, dtype=torch.float32, device=dev) if l.smooth else None)
+    _check(lib().moe_w8a8_linear_export(l.handle, out["wq"].data_ptr(), out["sw"].data_ptr(),
+                                        out["inv_s"].data_ptr() if l.smooth else None, _stream(stream)),
+           "moe_w8a8_linear_export")
+    return out
+
+
+def moe_w8a8_linear_check_status(l: Linear, stream=None):
+    _check(lib().moe_w8a8_linear_check_status(l.handle, _stream(stream)), "moe_w8a8_linear_check_status")
+
+
+def make_norm_config(d, in_dtype=MOE_BF16, res_dtype=MOE_BF16, out_dtype=MOE_BF16, gate=MOE_GATE_NONE,
+                     gate_sigmoid=False, eps=1e-6, residual_scale=1.0, branch_scale=1.0,
+                     weight_offset=0.0) -> moe_w8a8_norm_config:
+    return moe_w8a8_norm_config(d, in_dtype, res_dtype, out_dtype, gate, 1 if gate_sigmoid else 0, eps,
+                                residual_scale, branch_scale, weight_offset)
+
+
+def moe_w8a8_block_norm(cfg: moe_w8a8_norm_config, T: int, b=None, x=None, gate=None, w_post=None, w_pre=None,
+                        inv_s=None, x_out=None, n_out=None, xq=None, sx=None, stream=None):
+    if T == 0:
+        return
+    dev, d, f32 = _device(), cfg.d, _f32()
+    res = _types(cfg.res_dtype)
+    none = (None, 0)
+    gp, ldg = none
+    if gate is not None:
+        if cfg.gate == MOE_GATE_ELEMENT:
+            gp, ldg = _matrix(gate, T, d, "gate", _types(cfg.in_dtype), dev)
+        else:
+            gp = _vector(gate, T if cfg.gate == MOE_GATE_TOKEN else d, "gate", f32, dev)
+    io = moe_w8a8_norm_io(
+        *(none if b is None else _matrix(b, T, d, "b", _types(cfg.in_dtype), dev)),
+        *(none if x is None else _matrix(x, T, d, "x", res, dev)), gp, ldg, _vector(w_post, d, "w_post", f32, dev),
+        _vector(w_pre, d, "w_pre", f32, dev), _vector(inv_s, d, "inv_s", f32, dev),
+        *(none if x_out is None else _matrix(x_out, T, d, "x_out", res, dev)),
+        *(none if n_out is None else _matrix(n_out, T, d, "n_out", _types(cfg.out_dtype), dev)),
+        *(none if xq is None else _matrix(xq, T, d, "xq", (_torch().int8,), dev)), _vector(sx, T, "sx", f32, dev))
+    _check(lib().moe_w8a8_block_norm(ctypes.byref(cfg), ctypes.byref(io), T, _stream(stream)), "moe_w8a8_block_norm")
+
+
+def moe_w8a8_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, allowed=None, prob=None,
+                    stream=None):
+    torch = _torch()
+    dev, f32, i32 = _device(), _f32(), (torch.int32,)
+    rows, vocab = logits.shape
+    if rows == 0:
+        return
+    lp, ld = _matrix(logits, rows, vocab, "logits", (torch.float32, torch.bfloat16), dev)
+    ap, lda = (None, 0) if allowed is None else _matrix(allowed, rows, (vocab + 31) // 32, "allowed", i32, dev)
+    io = moe_w8a8_sample_io(
+        lp, ld, ap, lda, _vector(temperature, rows, "temperature", f32, dev), _vector(top_k, rows, "top_k", i32, dev),
+        _vector(top_p, rows, "top_p", f32, dev), _vector(min_p, rows, "min_p", f32, dev), _vector(u, rows, "u", f32, dev),
+        _vector(token, rows, "token", i32, dev), _vector(prob, rows, "prob", f32, dev))
+    _check(lib().moe_w8a8_sample(ctypes.byref(io), rows, vocab, MOE_BF16 if logits.dtype == torch.bfloat16 else MOE_F32,
+                                 _stream(stream)), "moe_w8a8_sample")
 
 
 # ------------------------------------------------------------------ measurement aid

@@ -249,4 +249,55 @@ cudaError_t launch_combine_blocked(const float* o_blocks, const int32_t* ts2row,
 // Bytes of one per-slot output value: the layer's output precision.
 inline size_t o_bytes(const moe_w8a8_config& c) { return c.out_dtype == MOE_BF16 ? 2 : 4; }
 
+// ------------------------------------------------------------------ around the layer
+
+// A dense product: weights as 8-bit codes in tiles of 128 channels x 128 inputs
+// (16 KB of contiguous memory each, [channel tile][input tile][channel][input];
+// channels padded to a multiple of 256 and inputs to one of 128 with zeros).
+struct LinearTiles {
+    int n, k, nb, kb;         // channels, inputs, channel tiles (even), input tiles
+    const int8_t* w;
+    const float* sw;          // [nb * 128], zeros past n
+    const float* bias;        // [nb * 128] or null
+    CUtensorMap tm_w;         // over w as rows of 128 bytes, boxes of 128 rows
+    int num_sms;
+    int32_t* status;
+};
+bool linear_make_map(LinearTiles* t);
+cudaError_t launch_linear_input_absmax(const float* w, int k, int n, float* aw, cudaStream_t s);
+cudaError_t launch_linear_quantize(const float* w, const float* smooth, const LinearTiles& t, int8_t* out, float* sw,
+                                   cudaStream_t s);
+cudaError_t launch_linear_tile(const int8_t* wq, const LinearTiles& t, int8_t* out, cudaStream_t s);
+cudaError_t launch_linear_untile(const LinearTiles& t, int8_t* wq, cudaStream_t s);
+cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, const float* sx, int T, void* y, int64_t ldy,
+                          int out_dtype, cudaStream_t s);
+
+struct NormParams {
+    int64_t T;
+    int d, in_dtype, res_dtype, out_dtype, gate_kind, gate_sigmoid;
+    float eps, residual_scale, branch_scale, weight_offset;
+    const void *b, *x, *gate;
+    const float *w_post, *w_pre, *inv_s;
+    void *x_out, *n_out;
+    int8_t* xq;
+    float* sx;
+    int64_t ldb, ldx, ldg, ldxo, ldn, ldq;
+};
+cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s);
+
+struct SampleParams {
+    const void* logits;
+    int64_t ld, ld_allowed;
+    int rows, vocab, dtype;
+    int per_block;            // set by the launch: tokens per thread block
+    const uint32_t* allowed;
+    const float* temperature;
+    const int32_t* top_k;
+    const float *top_p, *min_p, *u;
+    int32_t* token;
+    float* prob;
+};
+constexpr int kSampleMaxVocab = MOE_SAMPLE_MAX_VOCAB;
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t s);
+
 }  // namespace moe
