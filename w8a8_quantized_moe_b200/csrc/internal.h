@@ -298,6 +298,7 @@ struct SampleParams {
     float* prob;
 };
 constexpr int kSampleMaxVocab = MOE_SAMPLE_MAX_VOCAB;
+constexpr float kSampleMinTemperature = 1e-36f;   // log2(e) / temperature x 32 is finite above it
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t s);
 
 }  // namespace moe

@@ -19,7 +19,7 @@
 //     tokens that the top_p could reach, with their masses) names the bin where
 //     a prefix ends.
 //   - If the tokens down to that bin are few, the first block of the cluster
-//     gets them as a list, sorts it and finishes the row alone.
+//     gets them as a list and finishes the row alone.
 //   - Else it gets the tokens of that bin alone and finds the cut inside; the
 //     blocks then add up what lies above the cut, in the order of the tokens.
 //   - Where a bin holds more than a list takes (many equal logits), the cut is
@@ -38,95 +38,80 @@ constexpr int kSaThreads = 512;
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaMaxCluster = 8;
 constexpr int kMassBits = 45;
-constexpr uint32_t kNone = 0x007fffffu;   // ordered key of -infinity: a token that may not be chosen
 constexpr int kList = 2048;               // tokens of a list
-constexpr int kMassBins = 1024;           // bins of 1/32 of a power of two, the last one open
+constexpr int kShortList = 512;           // ranked by counting, else sorted
+constexpr int kMassBins = 1024;           // bins of 1/32 of a power of two
 constexpr int kKeyBins = 2048;            // bins of the selection by key bits
-// scratch of a block: the histograms (3 x kKeyBins words, or counts, low and high
-// sums of kMassBins), or a list of its own tokens and, in the first block, the row's
+// a block's scratch: a list of its own tokens and, in the first block, the row's
+// (or the 3 x kKeyBins words of the selection by key bits); then the histogram
 constexpr int kScratchWords = 2 * 2 * kList;
-static_assert(kScratchWords >= 3 * kKeyBins && kScratchWords >= 3 * kMassBins, "scratch");
+constexpr int kHistWords = 2 * kMassBins;
+static_assert(kScratchWords >= 3 * kKeyBins, "scratch");
+constexpr float kMagic = 12582912.0f;     // 1.5 x 2^23: adding it rounds to an integer in the low bits
 
-// Keys order like the logits: the sign bit set for values >= 0, all bits
-// inverted below.  -0 becomes +0, a NaN counts as -infinity.
+// Ordered integers of logits: the sign bit set for values >= 0, all bits
+// inverted below.  (Logits are kept with -0 as +0; what may not be chosen and
+// NaN as -infinity.)
 __device__ __forceinline__ uint32_t key_of(float v) {
-    if (!(v == v)) return kNone;
-    const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));
+    const uint32_t b = __float_as_uint(v);
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000u); }
 
-// Masses 2^x, x = (l - max) log2(e) / temperature.  x is formed in two fp32
-// parts (the difference and the product each with its rounding error), x = k /
-// 32 + r, and 2^x = 2^(k >> 5) T[k & 31] (1 + q) with a table of 2^(j / 32) in
-// 32 bits and q = e^(r ln 2) - 1 by its Taylor polynomial to degree 4 (|r ln 2|
-// < 0.011, remainder 2e-12): within 2e-9 of the true value, in integer and fp32
-// instructions alone.  (In fp64, with a polynomial of degree 9, a pass over 256
-// x 131072 tokens took several times as long.)
+// Masses 2^x, x = (l - max) c, c = log2(e) / temperature.  32 l c is rounded to an
+// integer k_l by one fused multiply-add; r = l c - k_l / 32 is another, exact but
+// for one rounding of a number below 1/64; with k_m and r_m of the largest logit,
+// 2^x = 2^(floor(k / 32)) T[k mod 32] (1 + q), k = k_l - k_m, T[j] = 2^(j / 32) in
+// 31 bits and q = 2^(r - r_m) - 1 by its Taylor polynomial to degree 4 (remainder
+// 4e-11): within 3e-9 of the true value, in fp32 and integer instructions.  (With
+// fp64 and a polynomial of degree 9, 256 x 131072 tokens took 4 times as long.)
+// Where |max c| is too large for k_l, l - max takes the place of l; it is exact
+// for every token whose mass is not far below the smallest unit.
 struct Softmax {
-    uint32_t kmax;
-    float m, c, c_lo;
-    double cd;
-    const uint32_t* tab;   // shared: round(2^(31 + j / 32))
-    __device__ __forceinline__ void init(uint32_t key_max, float temperature, const uint32_t* table) {
-        kmax = key_max;
-        m = value_of(key_max);
+    float shift, c, c32, c_lo, rm, t_max;   // t_max: kMagic + k_m
+    double m, cd;
+    const uint32_t* tab;                    // shared: round(2^(30 + j / 32))
+    __device__ __forceinline__ void init(float max_logit, float temperature, const uint32_t* table) {
+        m = (double)max_logit;
         cd = 1.4426950408889634074 / (double)temperature;
-        c = (float)fmin(cd, 3e38);
-        c_lo = (float)(fmin(cd, 3e38) - (double)c);
+        c = (float)cd;
+        c_lo = (float)(cd - (double)c);
+        c32 = c * 32.0f;
+        shift = fabs(m * cd) > 65536.0 ? max_logit : 0.0f;
+        t_max = place(max_logit);
+        rm = (float)((m - (double)shift) * cd - (double)(t_max - kMagic) / 32.0);
         tab = table;
     }
-    // k and the 32-bit mantissa M (in units of 2^-31): mass M 2^(k >> 5); false
-    // below 2^-1000.
-    __device__ __forceinline__ bool parts(uint32_t key, int& k, uint32_t& M) const {
-        const float l = value_of(key);
-        const float s = __fsub_rn(l, m), b = __fsub_rn(s, l);
-        const float err = __fadd_rn(__fsub_rn(l, __fsub_rn(s, b)), __fsub_rn(-m, b));
-        const float xh = __fmul_rn(s, c);
-        if (key == kmax) {
-            k = 0;
-            M = 1u << 31;
-            return true;
-        }
-        if (!(xh > -1000.0f)) return false;
-        const float xl = __fadd_rn(__fmaf_rn(s, c, -xh), __fmaf_rn(s, c_lo, __fmul_rn(err, c)));
-        const float t = __fmaf_rn(xh, 32.0f, 12582912.0f);   // 1.5 x 2^23: rounds to an integer in the low bits
-        k = __float_as_int(t) - 0x4b400000;
-        const float r = __fadd_rn(__fmaf_rn(__fsub_rn(t, 12582912.0f), -0.03125f, xh), xl);
-        const float y = __fmul_rn(r, 0.693147180559945f);
-        float p = __fmaf_rn(y, 1.0f / 24, 1.0f / 6);
-        p = __fmaf_rn(p, y, 0.5f);
-        p = __fmaf_rn(__fmul_rn(p, y), y, y);
-        const uint32_t T = tab[k & 31];
+    // kMagic + k_l: falls with the logit, -infinity for tokens that take no part
+    __device__ __forceinline__ float place(float l) const { return __fmaf_rn(__fsub_rn(l, shift), c32, kMagic); }
+    __device__ __forceinline__ int bin(float t) const { return (int)__fsub_rn(t_max, t); }
+    // the 31-bit mantissa (units of 2^-30) of a token at place t, at least t_max - 2^15
+    __device__ __forceinline__ uint32_t mantissa(float l, float t) const {
+        const float lr = __fsub_rn(l, shift);
+        float r = __fmaf_rn(lr, c, __fmul_rn(__fsub_rn(t, kMagic), -0.03125f));
+        r = __fsub_rn(__fmaf_rn(lr, c_lo, r), rm);
+        float p = __fmaf_rn(r, 0.00961812910763f, 0.0555041086648f);   // ln2^4 / 24, ln2^3 / 6
+        p = __fmaf_rn(p, r, 0.240226506959f);                          // ln2^2 / 2
+        p = __fmaf_rn(p, r, 0.693147180560f);
+        p = __fmul_rn(p, r);
+        const uint32_t T = tab[(__float_as_int(t) - __float_as_int(t_max)) & 31];
         const int q = __float2int_rn(__fmul_rn(p, 4294967296.0f));
-        M = T + (uint32_t)(((int64_t)(uint64_t)T * q) >> 32);
-        return true;
+        return T + (uint32_t)(int)(((int64_t)(uint64_t)T * q) >> 32);
     }
-    static __device__ __forceinline__ uint64_t fixed(int k, uint32_t M) {
-        const int n = -(k >> 5);
-        const uint64_t v = n < 64 ? ((uint64_t)M << (kMassBits - 31)) >> n : 0;
-        return v ? v : 1;
+    // in units of 2^-45, for a token `below` places under the largest
+    static __device__ __forceinline__ uint64_t fixed(uint32_t M, int below) {
+        return ((uint64_t)M << (kMassBits - 30)) >> ((below + 31) >> 5);
     }
-    __device__ __forceinline__ uint64_t mass(uint32_t key) const {
-        int k;
-        uint32_t M;
-        return parts(key, k, M) ? fixed(k, M) : 0;
-    }
-    // the bin of a token: tokens of a lower bin have a larger logit
-    __device__ __forceinline__ int bin(uint32_t key) const {
-        if (key == kmax) return 0;
-        const float xh = __fmul_rn(__fsub_rn(value_of(key), m), c);
-        if (!(xh > -1000.0f)) return kMassBins - 1;
-        const int k = __float_as_int(__fmaf_rn(xh, 32.0f, 12582912.0f)) - 0x4b400000;
-        return min(-k, kMassBins - 1);
+    __device__ __forceinline__ uint64_t mass(float l) const {
+        const float t = place(l);
+        if (!(t >= t_max - 46.0f * 32)) return t >= t_max - 32000.0f ? 1 : 0;
+        return max(fixed(mantissa(l, t), bin(t)), (uint64_t)1);
     }
     // the mass in 64 bits, for the chosen token's probability
-    __device__ __forceinline__ double exact(uint32_t key) const {
-        if (key == kmax) return 1.0;
-        return exp2(((double)value_of(key) - (double)m) * cd);
-    }
+    __device__ __forceinline__ double exact(float l) const { return exp2(((double)l - m) * cd); }
 };
 
 __device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
@@ -144,21 +129,24 @@ __device__ __forceinline__ uint64_t warp_scan_u64(uint64_t v, int lane) {   // i
 }
 
 struct SaShared {
-    uint64_t slots[2][kSaMaxCluster];   // per reduction, alternating: one value per block
+    uint64_t slots[2][kSaMaxCluster];     // per reduction, alternating: one value per block
     uint64_t warp_sum[kSaWarps];
-    uint64_t found_above, found_need;
-    uint32_t found, cut_key;
+    uint64_t coarse[32], total;           // this block's histogram by powers of two, and its mass
+    uint64_t gather[2][kSaMaxCluster][32], gather_total[kSaMaxCluster];
+    uint64_t found_above;
+    uint32_t found;
+    float cut_value;
     int32_t cut_index;
-    uint32_t list_base, list_count;     // list_count: of the row, in the first block
+    uint32_t list_base, list_count[2];    // list_count: of the row's lists, in the first block
     uint32_t own_count;
     uint32_t tab[32];
 };
 
-// The tokens still in the running: key above K, or equal to K and below index I.
+// The tokens still in the running: logit above K, or equal to K and index below I.
 struct Cut {
-    uint32_t K;
+    float K;
     int I;
-    __device__ __forceinline__ bool in(uint32_t key, int index) const { return key > K || (key == K && index < I); }
+    __device__ __forceinline__ bool in(float l, int index) const { return l > K || (l == K && index < I); }
 };
 
 // One row of a cluster.
@@ -166,8 +154,9 @@ struct Row {
     cg::cluster_group cl;
     int nb, rank;                // blocks of the cluster, this one
     SaShared* sh;
-    uint32_t* keys;              // this block's tokens [lo, lo + n), kNone up to a multiple of 4
+    float* logits;               // this block's tokens [lo, lo + n), -infinity up to a multiple of 4
     uint32_t* scratch;
+    uint32_t* hist;
     int lo, n, per_warp;         // a warp owns tokens [warp * per_warp, + per_warp) of the block's
     int turn;
     int tid, lane, warp;
@@ -193,8 +182,8 @@ struct Row {
         turn ^= 1;
         return total;
     }
-    __device__ uint32_t max_key(uint32_t k) {
-        k = __reduce_max_sync(0xffffffffu, k);
+    __device__ float max_logit(float v) {
+        uint32_t k = __reduce_max_sync(0xffffffffu, key_of(v));
         if (lane == 0) sh->warp_sum[warp] = k;
         __syncthreads();
         if (warp == 0) {
@@ -205,13 +194,15 @@ struct Row {
         k = 0;
         for (int i = 0; i < nb; ++i) k = max(k, (uint32_t)sh->slots[turn][i]);
         turn ^= 1;
-        return k;
+        return value_of(k);
     }
-    // A block's last step: the others leave, the first one when none of them
-    // reads its shared memory any more.
-    __device__ void leave() {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        if (rank == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // Sum over the threads of the block.
+    __device__ uint64_t block_sum(uint64_t v) {
+        v = warp_sum_u64(v);
+        __syncthreads();
+        if (lane == 0) sh->warp_sum[warp] = v;
+        __syncthreads();
+        return warp_sum_u64(lane < kSaWarps ? sh->warp_sum[lane] : 0);
     }
     // Inclusive scan of v over the threads of the block.
     __device__ uint64_t block_scan(uint64_t v) {
@@ -222,15 +213,21 @@ struct Row {
         for (int w = 0; w < warp; ++w) v += sh->warp_sum[w];
         return v;
     }
+    // A block's last step: the others leave, the first one when none of them
+    // reads its shared memory any more.
+    __device__ void leave() {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        if (rank == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
 };
 
 // ------------------------------------------------------------------ selection by key bits
 
-// Among the tokens inside `cut`, in order of falling key: the key at which the
-// running count (or mass) reaches `need`, and how much lies strictly above it.
-// False when the whole set does not reach it.
+// Among the tokens inside `cut`, in order of falling logit: the one at which
+// the running count (or mass) reaches `need`, and how much lies strictly above
+// it.  False when the whole set does not reach it.
 template <bool MASS>
-__device__ __noinline__ bool select_key(Row& r, const Softmax& sm, const Cut& cut, double need, uint32_t& key_out,
+__device__ __noinline__ bool select_key(Row& r, const Softmax& sm, const Cut& cut, double need, float& value_out,
                                         uint64_t& above_out) {
     constexpr int kPer = kKeyBins / kSaThreads;
     uint32_t prefix = 0, mask = 0;
@@ -242,12 +239,13 @@ __device__ __noinline__ bool select_key(Row& r, const Softmax& sm, const Cut& cu
         for (int i = r.tid; i < (MASS ? 3 : 1) * kKeyBins; i += kSaThreads) h[i] = 0;
         __syncthreads();
         for (int i = r.tid; i < r.n; i += kSaThreads) {
-            const uint32_t k = r.keys[i];
-            if ((k & mask) != prefix || !cut.in(k, r.lo + i)) continue;
+            const float l = r.logits[i];
+            const uint32_t k = key_of(l);
+            if ((k & mask) != prefix || !cut.in(l, r.lo + i)) continue;
             const int bin = (k >> shift) & (bins - 1);
             if constexpr (MASS) {
                 // 15 bits at a time: 2^15 tokens of a block cannot overflow a sum
-                const uint64_t m = sm.mass(k);
+                const uint64_t m = sm.mass(l);
                 if (m & 0x7fffu) atomicAdd(&h[bin], (uint32_t)(m & 0x7fffu));
                 if ((m >> 15) & 0x7fffu) atomicAdd(&h[kKeyBins + bin], (uint32_t)((m >> 15) & 0x7fffu));
                 if (m >> 30) atomicAdd(&h[2 * kKeyBins + bin], (uint32_t)(m >> 30));
@@ -289,18 +287,18 @@ __device__ __noinline__ bool select_key(Row& r, const Softmax& sm, const Cut& cu
         prefix |= bin << shift;
         mask |= (uint32_t)(bins - 1) << shift;
     }
-    key_out = prefix;
+    value_out = value_of(prefix);
     above_out = above;
     return true;
 }
 
 // The index of the tie number `keep` (from 0, in the order of the tokens) among
-// the tokens inside `cut` whose key is K: the first one left out; `none` when
+// the tokens inside `cut` whose logit is K: the first one left out; `none` when
 // there are not that many.
-__device__ __noinline__ int tie_limit(Row& r, const Cut& cut, uint32_t K, uint64_t keep, int none) {
+__device__ __noinline__ int tie_limit(Row& r, const Cut& cut, float K, uint64_t keep, int none) {
     const int w0 = r.warp * r.per_warp, w1 = min(r.n, w0 + r.per_warp);
     uint32_t c = 0;
-    for (int i = w0 + r.lane; i < w1; i += 32) c += r.keys[i] == K && cut.in(K, r.lo + i);
+    for (int i = w0 + r.lane; i < w1; i += 32) c += r.logits[i] == K && cut.in(K, r.lo + i);
     const uint64_t mine = warp_sum_u64(c);
     uint64_t before;
     if (r.sum(c, before) <= keep) return none;
@@ -313,7 +311,7 @@ __device__ __noinline__ int tie_limit(Row& r, const Cut& cut, uint32_t K, uint64
         uint64_t at = before;
         for (int i0 = w0; i0 < w1; i0 += 32) {
             const int i = i0 + r.lane;
-            const bool is = i < w1 && r.keys[i] == K && cut.in(K, r.lo + i);
+            const bool is = i < w1 && r.logits[i] == K && cut.in(K, r.lo + i);
             const uint32_t m = __ballot_sync(0xffffffffu, is);
             if (keep < at + __popc(m)) {
                 if (is && __popc(m & ((1u << r.lane) - 1)) == (int)(keep - at)) r.sh->cut_index = r.lo + i;
@@ -330,7 +328,7 @@ __device__ __noinline__ int tie_limit(Row& r, const Cut& cut, uint32_t K, uint64
 
 // The first top_k tokens inside `cut`, by key bits.
 __device__ __noinline__ void cut_count(Row& r, const Softmax& sm, Cut& cut, int top_k, int vocab) {
-    uint32_t K = 0;
+    float K = 0;
     uint64_t above = 0;
     if (!select_key<false>(r, sm, cut, (double)top_k, K, above)) return;
     cut = Cut{K, tie_limit(r, cut, K, (uint64_t)top_k - above, vocab)};
@@ -338,7 +336,7 @@ __device__ __noinline__ void cut_count(Row& r, const Softmax& sm, Cut& cut, int 
 
 // The shortest prefix of the tokens inside `cut` whose mass reaches `need`, by key bits.
 __device__ __noinline__ void cut_mass(Row& r, const Softmax& sm, Cut& cut, double need, int vocab) {
-    uint32_t K = 0;
+    float K = 0;
     uint64_t above = 0;
     if (!select_key<true>(r, sm, cut, need, K, above)) return;
     const uint64_t ties = (uint64_t)fmax(1.0, ceil((need - (double)above) / (double)sm.mass(K)));
@@ -349,33 +347,41 @@ __device__ __noinline__ void cut_mass(Row& r, const Softmax& sm, Cut& cut, doubl
 // ------------------------------------------------------------------ lists
 
 // Entries order by falling logit, then rising index.
-__device__ __forceinline__ uint64_t entry_of(uint32_t key, int index) { return ((uint64_t)key << 32) | (uint32_t)~index; }
-__device__ __forceinline__ uint32_t entry_key(uint64_t e) { return (uint32_t)(e >> 32); }
+__device__ __forceinline__ uint64_t entry_of(float l, int index) { return ((uint64_t)key_of(l) << 32) | (uint32_t)~index; }
+__device__ __forceinline__ float entry_logit(uint64_t e) { return value_of((uint32_t)(e >> 32)); }
 __device__ __forceinline__ int entry_index(uint64_t e) { return (int)~(uint32_t)e; }
 
-// The row's tokens of bins [b0, b1] as a list in the first block's scratch
-// (second half).  Returns how many there are; more than kList: the list is
-// incomplete.  Every block calls it; `list_count` was cleared before the last
-// cluster barrier.
-__device__ uint32_t make_list(Row& r, const Softmax& sm, int b0, int b1) {
+// The row's tokens at places [t0, t1] as list number `which` in the first
+// block's scratch (second half).  Returns how many there are; more than kList:
+// the list is incomplete.
+__device__ uint32_t make_list(Row& r, const Softmax& sm, float t0, float t1, int which) {
     uint64_t* own = reinterpret_cast<uint64_t*>(r.scratch);
+    __syncthreads();
     if (r.tid == 0) r.sh->own_count = 0;
     __syncthreads();
+#pragma unroll 2
     for (int i = r.tid * 4; i < r.n; i += kSaThreads * 4) {
-        const uint4 q = *reinterpret_cast<const uint4*>(r.keys + i);
-        const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+        const float4 q = *reinterpret_cast<const float4*>(r.logits + i);
+        const float l[4] = {q.x, q.y, q.z, q.w};
+        bool in[4], any = false;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (k[j] <= kNone) continue;
-            const int b = sm.bin(k[j]);
-            if (b < b0 || b > b1) continue;
-            const uint32_t at = atomicAdd(&r.sh->own_count, 1u);
-            if (at < kList) own[at] = entry_of(k[j], r.lo + i + j);
+            const float t = sm.place(l[j]);
+            in[j] = t >= t0 && t <= t1;
+            any |= in[j];
+        }
+        if (any) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in[j] && l[j] > minus_inf()) {
+                    const uint32_t at = atomicAdd(&r.sh->own_count, 1u);
+                    if (at < kList) own[at] = entry_of(l[j], r.lo + i + j);
+                }
         }
     }
     __syncthreads();
     const uint32_t count = r.sh->own_count;
-    uint32_t* row_count = r.cl.map_shared_rank(&r.sh->list_count, 0);
+    uint32_t* row_count = r.cl.map_shared_rank(&r.sh->list_count[which], 0);
     if (r.tid == 0) r.sh->list_base = count ? atomicAdd(row_count, count) : 0;
     __syncthreads();
     uint64_t* list = r.cl.map_shared_rank(own + kList, 0);
@@ -422,7 +428,7 @@ __device__ void running_mass(Row& r, const Softmax& sm, const uint64_t* list, in
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int i = r.tid * kPer + j;
-        v[j] = i < count ? sm.mass(entry_key(list[i])) : 0;
+        v[j] = i < count ? sm.mass(entry_logit(list[i])) : 0;
         mine += v[j];
     }
     uint64_t at = above + r.block_scan(mine) - mine;
@@ -450,39 +456,79 @@ __device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
     return min(t, total - 1);
 }
 
-__device__ void choose(const SampleParams& p, const Softmax& sm, int row, int index, uint32_t key, uint64_t total) {
+__device__ void choose(const SampleParams& p, const Softmax& sm, int row, int index, float l, uint64_t total) {
     p.token[row] = index;
-    if (p.prob) p.prob[row] = (float)(sm.exact(key) * (double)(1ull << kMassBits) / (double)total);
+    if (p.prob) p.prob[row] = (float)(sm.exact(l) * (double)(1ull << kMassBits) / (double)total);
 }
 
-// Finish a row whose tokens in the running are all in the list, by the first block alone.
+// Finish a row whose tokens in the running are all in the list, by the first
+// block alone.  top_p < 1: the prefix reaches `need`, or (top_k > 0) top_p of
+// the mass of the first top_k.
 __device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int count, int top_k, float top_p,
-                            double min_mass) {
-    uint64_t* list = sorted_list(r, count);
+                            double need, float min_logit) {
     uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
+    if (count <= kShortList) {
+        // by counting: `parts` neighbouring threads per entry add up what precedes it
+        uint64_t* list = run + kList;
+        const int parts = kSaThreads / max(pow2_at_least(count), 16);
+        const int i = r.tid / parts, part = r.tid % parts;
+        const uint64_t mine = i < count ? list[i] : 0;
+        const uint64_t mass = i < count ? sm.mass(entry_logit(mine)) : 0;
+        if (part == 0 && i < count) run[i] = mass;
+        __syncthreads();
+        uint64_t before = 0;
+        int rank = 0;
+        if (i < count)
+            for (int j = part; j < count; j += parts)
+                if (list[j] > mine) {
+                    ++rank;
+                    before += run[j];
+                }
+        for (int o = parts >> 1; o >= 1; o >>= 1) {
+            rank += __shfl_xor_sync(0xffffffffu, rank, o);
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+        }
+        const bool own = part == 0 && i < count;
+        bool in = own && (top_k <= 0 || rank < top_k);
+        if (top_p < 1.0f) {
+            if (top_k > 0) need = fmax((double)top_p * (double)r.block_sum(in ? mass : 0), 1.0);
+            in = in && (rank == 0 || (double)before < need);
+        }
+        in = in && (rank == 0 || entry_logit(mine) >= min_logit);
+        const uint64_t total = r.block_sum(in ? mass : 0);   // (its barriers end the reads of run)
+        if (own) run[i] = in ? mass : 0;
+        const uint64_t target = target_of(p.u[row], total);
+        __syncthreads();
+        // in the order of the tokens: ~index falls as the index rises
+        uint64_t sum = 0;
+        if (i < count)
+            for (int j = part; j < count; j += parts)
+                if ((uint32_t)list[j] > (uint32_t)mine) sum += run[j];
+        for (int o = parts >> 1; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (in && sum <= target && target < sum + mass) choose(p, sm, row, entry_index(mine), entry_logit(mine), total);
+        return;
+    }
+    uint64_t* list = sorted_list(r, count);
     int n = top_k > 0 ? min(count, top_k) : count;
     running_mass(r, sm, list, n, 0, run);
-    // need: given, or (by the list alone) top_p of its mass
     if (top_p < 1.0f) {
-        const double need = top_k > 0 ? fmax((double)top_p * (double)run[n - 1], 1.0) : __longlong_as_double(r.sh->found_need);
+        if (top_k > 0) need = fmax((double)top_p * (double)run[n - 1], 1.0);
         n = prefix_reaching(r, run, n, need);
     }
-    if (min_mass > 0.0) {
-        if (r.tid == 0) r.sh->found = n;
-        __syncthreads();
-        for (int i = r.tid; i < n; i += kSaThreads)
-            if ((double)sm.mass(entry_key(list[i])) < min_mass) atomicMin(&r.sh->found, (uint32_t)i);
-        __syncthreads();
-        n = max(1, (int)r.sh->found);
-    }
+    if (r.tid == 0) r.sh->found = n;
+    __syncthreads();
+    for (int i = r.tid; i < n; i += kSaThreads)
+        if (entry_logit(list[i]) < min_logit) atomicMin(&r.sh->found, (uint32_t)i);
+    __syncthreads();
+    n = max(1, (int)r.sh->found);
     const uint64_t total = run[n - 1];
     const uint64_t target = target_of(p.u[row], total);
-    // in the order of the tokens: entries with the index on top, sorted again
+    // in the order of the tokens: entries with ~index on top, sorted again
     __syncthreads();
     const int m = pow2_at_least(n);
     for (int i = r.tid; i < m; i += kSaThreads) {
         const uint64_t e = list[i];
-        list[i] = i < n ? (e << 32) | (e >> 32) : 0;   // ~index falls as the index rises
+        list[i] = i < n ? (e << 32) | (e >> 32) : 0;
     }
     sort_falling(list, m, r.tid);
     for (int i = r.tid; i < n; i += kSaThreads) list[i] = (list[i] << 32) | (list[i] >> 32);
@@ -490,48 +536,66 @@ __device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, in
     running_mass(r, sm, list, n, 0, run);
     for (int i = r.tid; i < n; i += kSaThreads)
         if (run[i] > target && (i == 0 || run[i - 1] <= target))
-            choose(p, sm, row, entry_index(list[i]), entry_key(list[i]), total);
+            choose(p, sm, row, entry_index(list[i]), entry_logit(list[i]), total);
 }
 
-// ------------------------------------------------------------------ the histogram of masses
+// ------------------------------------------------------------------ the histogram
 
-// The first bin at which the running count (or mass) of the row's histogram
-// reaches `need`, what lies above it, or kMassBins when it does not.  All
-// blocks; the histograms are complete (a cluster barrier has passed).
+// What a block's histogram holds of one bin: its count, or its mass.
 template <bool MASS>
-__device__ int find_bin(Row& r, double need, uint64_t& above) {
-    constexpr int kPer = kMassBins / kSaThreads;
-    uint64_t v[kPer], mine = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int bin = r.tid * kPer + j;
-        uint64_t s = 0;
-        for (int b = 0; b < r.nb; ++b) {
-            const uint32_t* h = r.cl.map_shared_rank(r.scratch, b);
-            s += h[bin];
-            if constexpr (MASS) s += (uint64_t)h[kMassBins + bin] << 16;
-        }
-        if constexpr (MASS) {
-            // sums of mantissas of masses 2^-n: at most 2^50, or 2^49 where n = 0
-            const int n = (bin + 31) >> 5;
-            s = (s << (kMassBits - 31)) >> n;
-        }
-        v[j] = s;
-        mine += s;
+__device__ __forceinline__ uint64_t bin_value(const uint32_t* h, int bin) {
+    if constexpr (!MASS) return h[bin];
+    // sums of mantissas below 2^31 of at most 2^15 tokens, of masses 2^-n
+    const uint64_t s = (uint64_t)h[bin] + ((uint64_t)h[kMassBins + bin] << 16);
+    return (s << (kMassBits - 30)) >> ((bin + 31) >> 5);
+}
+
+// The bin at which the running count (or mass) of the row reaches `need`, and
+// what lies above it; kMassBins when it does not.  `own`: this thread's part of
+// the row's mass, whose sum is `total`; need is top_p of it, or given.  Two
+// levels, so that a block reads 64 words of each other one's shared memory: the
+// sums over powers of two, then the 32 bins of one of them.
+template <bool MASS>
+__device__ int find_bin(Row& r, uint64_t own, float top_p, double& need, uint64_t& total, uint64_t& above) {
+    const uint64_t mine = r.block_sum(own);   // (its barriers complete the histogram)
+    for (int g = r.warp; g < 32; g += kSaWarps) {
+        const uint64_t s = warp_sum_u64(bin_value<MASS>(r.hist, g * 32 + r.lane));
+        if (r.lane == 0) r.sh->coarse[g] = s;
     }
-    if (r.tid == 0) r.sh->found = kMassBins;
-    uint64_t before = r.block_scan(mine) - mine;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        if ((double)before < need && (double)(before + v[j]) >= need) {
-            r.sh->found = (uint32_t)(r.tid * kPer + j);
-            r.sh->found_above = before;
-        }
-        before += v[j];
+    if (r.tid == 0) r.sh->total = mine;
+    r.cl.sync();
+    if (r.warp < r.nb) {
+        const SaShared* from = r.cl.map_shared_rank(r.sh, r.warp);
+        r.sh->gather[0][r.warp][r.lane] = from->coarse[r.lane];
+        if (r.lane == 0) r.sh->gather_total[r.warp] = from->total;
     }
     __syncthreads();
-    above = r.sh->found_above;
-    return (int)r.sh->found;
+    uint64_t s = 0;
+    total = 0;
+    for (int b = 0; b < r.nb; ++b) {
+        s += r.sh->gather[0][b][r.lane];
+        total += r.sh->gather_total[b];
+    }
+    if (MASS) need = fmax((double)top_p * (double)total, 1.0);
+    uint64_t inc = warp_scan_u64(s, r.lane);
+    uint32_t at = __ballot_sync(0xffffffffu, (double)inc >= need);
+    if (!at) return kMassBins;
+    const int g = __ffs(at) - 1;
+    above = __shfl_sync(0xffffffffu, inc - s, g);
+    if (r.warp < r.nb)
+        r.sh->gather[1][r.warp][r.lane] = bin_value<MASS>(r.cl.map_shared_rank(r.hist, r.warp), g * 32 + r.lane);
+    __syncthreads();
+    s = 0;
+    for (int b = 0; b < r.nb; ++b) s += r.sh->gather[1][b][r.lane];
+    inc = above + warp_scan_u64(s, r.lane);
+    at = __ballot_sync(0xffffffffu, (double)inc >= need);
+    const int j = __ffs(at) - 1;   // the bins of g add up to its sum: one is found
+    above = __shfl_sync(0xffffffffu, inc - s, j);
+    return g * 32 + j;
+}
+
+__device__ __forceinline__ float clean(float v, bool allowed) {
+    return allowed && v == v ? __fadd_rn(v, 0.0f) : minus_inf();
 }
 
 template <bool VEC>
@@ -544,7 +608,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
     r.rank = (int)r.cl.block_rank();
     r.sh = &shared;
     r.scratch = sa_smem;
-    r.keys = sa_smem + kScratchWords;
+    r.hist = sa_smem + kScratchWords;
+    r.logits = reinterpret_cast<float*>(sa_smem + kScratchWords + kHistWords);
     r.tid = threadIdx.x;
     r.lane = threadIdx.x & 31;
     r.warp = threadIdx.x >> 5;
@@ -553,61 +618,57 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
     r.lo = min(p.vocab, r.rank * p.per_block);
     r.n = min(p.vocab, r.lo + p.per_block) - r.lo;
     r.per_warp = p.per_block / kSaWarps;
-    if (r.tid < 32) shared.tab[r.tid] = (uint32_t)rint(exp2(31.0 + r.tid / 32.0));
-    if (r.tid == 0) shared.list_count = 0;
-    for (int i = r.tid; i < 3 * kMassBins; i += kSaThreads) r.scratch[i] = 0;
+    if (r.tid < 32) shared.tab[r.tid] = (uint32_t)rint(exp2(30.0 + r.tid / 32.0));
+    if (r.tid < 2) shared.list_count[r.tid] = 0;
+    for (int i = r.tid; i < kHistWords; i += kSaThreads) r.hist[i] = 0;
     pdl_wait();
 
-    // the row's logits, as keys, into shared memory
+    // the row's logits into shared memory
     const int64_t base = (int64_t)row * p.ld + r.lo;
     const uint32_t* allowed = p.allowed ? p.allowed + (int64_t)row * p.ld_allowed : nullptr;
-    uint32_t own_max = 0;
+    float own_max = minus_inf();
     if constexpr (VEC) {
 #pragma unroll 4
         for (int g = r.tid; g < (r.n + 7) / 8; g += kSaThreads) {
-            uint32_t k[8];
+            float v[8];
             if (g * 8 + 8 <= r.n) {
-                float v[8];
                 load8_act(p.logits, base + g * 8, p.dtype, v);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) k[c] = key_of(v[c]);
             } else {
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
-                    k[c] = g * 8 + c < r.n
-                               ? key_of(p.dtype == MOE_BF16
-                                            ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[base + g * 8 + c])
-                                            : reinterpret_cast<const float*>(p.logits)[base + g * 8 + c])
-                               : kNone;
+                    v[c] = g * 8 + c < r.n
+                               ? (p.dtype == MOE_BF16
+                                      ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[base + g * 8 + c])
+                                      : reinterpret_cast<const float*>(p.logits)[base + g * 8 + c])
+                               : minus_inf();
             }
             const int i0 = r.lo + g * 8;   // a multiple of 8
             const uint32_t bits = allowed ? allowed[i0 >> 5] >> (i0 & 31) : 0xffu;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                k[c] = (bits >> c) & 1u ? k[c] : kNone;
-                own_max = max(own_max, k[c]);
+                v[c] = clean(v[c], (bits >> c) & 1u);
+                own_max = fmaxf(own_max, v[c]);
             }
-            reinterpret_cast<uint4*>(r.keys)[2 * g] = make_uint4(k[0], k[1], k[2], k[3]);
-            reinterpret_cast<uint4*>(r.keys)[2 * g + 1] = make_uint4(k[4], k[5], k[6], k[7]);
+            reinterpret_cast<float4*>(r.logits)[2 * g] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(r.logits)[2 * g + 1] = make_float4(v[4], v[5], v[6], v[7]);
         }
     } else {
 #pragma unroll 4
         for (int i = r.tid; i < r.n; i += kSaThreads) {
-            uint32_t k = key_of(p.dtype == MOE_BF16 ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[base + i])
-                                                    : reinterpret_cast<const float*>(p.logits)[base + i]);
-            if (allowed && !((allowed[(r.lo + i) >> 5] >> ((r.lo + i) & 31)) & 1u)) k = kNone;
-            r.keys[i] = k;
-            own_max = max(own_max, k);
+            const float v = p.dtype == MOE_BF16 ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[base + i])
+                                                : reinterpret_cast<const float*>(p.logits)[base + i];
+            r.logits[i] = clean(v, !allowed || ((allowed[(r.lo + i) >> 5] >> ((r.lo + i) & 31)) & 1u));
+            own_max = fmaxf(own_max, r.logits[i]);
         }
-        if (r.tid < (-r.n & 3)) r.keys[r.n + r.tid] = kNone;
+        if (r.tid < (-r.n & 3)) r.logits[r.n + r.tid] = minus_inf();
     }
-    const float temp = p.temperature ? p.temperature[row] : 1.0f;
+    const float temp = p.temperature ? fminf(p.temperature[row], 3e38f) : 1.0f;
     const int top_k = p.top_k ? p.top_k[row] : 0;
     const float top_p = p.top_p ? p.top_p[row] : 1.0f;
-    const float mp = p.min_p ? p.min_p[row] : 0.0f;
-    const uint32_t kmax = r.max_key(own_max);
+    const float min_p = p.min_p ? p.min_p[row] : 0.0f;
+    float top = r.max_logit(own_max);
     const bool writer = r.rank == 0 && r.tid == 0;
-    if (kmax <= kNone) {   // nothing may be chosen
+    if (top == minus_inf()) {   // nothing may be chosen
         if (writer) {
             p.token[row] = -1;
             if (p.prob) p.prob[row] = 0.0f;
@@ -615,8 +676,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         r.cl.sync();
         return;
     }
-    if (!(temp > 0.0f)) {   // greedy: the lowest index among the largest
-        const int at = tie_limit(r, Cut{kNone, 0}, kmax, 0, 0);
+    if (!(temp > kSampleMinTemperature)) {   // greedy: the lowest index among the largest
+        const int at = tie_limit(r, Cut{minus_inf(), 0}, top, 0, 0);
         if (writer) {
             p.token[row] = at;
             if (p.prob) p.prob[row] = 1.0f;
@@ -624,114 +685,123 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         r.cl.sync();
         return;
     }
+    if (top == -minus_inf()) {   // infinities share the mass, nothing else has any
+        __syncthreads();
+        for (int i = r.tid; i < (r.n + 3) / 4 * 4; i += kSaThreads) r.logits[i] = r.logits[i] == top ? 0.0f : minus_inf();
+        own_max = own_max == top ? 0.0f : minus_inf();
+        top = 0.0f;
+        __syncthreads();
+    }
     Softmax sm;
-    sm.init(kmax, temp, shared.tab);
-    const double min_mass = mp > 0.0f ? fmin((double)mp, 1.0) * (double)(1ull << kMassBits) : 0.0;
-    Cut cut{kNone, 0};   // every token that may be chosen
-    uint32_t* hist = r.scratch;
-    bool cut_p = top_p < 1.0f;
+    sm.init(top, temp, shared.tab);
+    // e >= min_p as a bound on the logit (half a step of 1 in 64 bits counts as equal)
+    const float min_logit =
+        min_p > 0.0f ? fminf(top, __double2float_ru(sm.m + (double)temp * (log(fmin((double)min_p, 1.0)) - 1.2e-16)))
+                     : minus_inf();
+    Cut cut{minus_inf(), 0};   // every token that may be chosen
 
     if (top_k > 0) {
         // a bin that the top_k tokens do not go below: from the threads' largest tokens
         // while these are at least four times as many, else from all tokens
-        const bool by_thread = top_k <= r.nb * kSaThreads / 4;
-        if (by_thread) {
-            if (own_max > kNone) atomicAdd(&hist[sm.bin(own_max)], 1u);
+        auto count = [&](float l) {
+            const float t = sm.place(l);
+            if (t > sm.t_max - (float)kMassBins) atomicAdd(&r.hist[sm.bin(t)], 1u);
+        };
+        if (top_k <= r.nb * kSaThreads / 4) {
+            count(own_max);
         } else {
-            for (int i = r.tid; i < r.n; i += kSaThreads)
-                if (r.keys[i] > kNone) atomicAdd(&hist[sm.bin(r.keys[i])], 1u);
+            for (int i = r.tid; i < r.n; i += kSaThreads) count(r.logits[i]);
         }
-        r.cl.sync();
-        uint64_t above;
-        const int b = min(find_bin<false>(r, (double)top_k, above), kMassBins - 1);
-        r.cl.sync();   // the histograms have been read: the scratch is free
-        const uint32_t count = make_list(r, sm, 0, b);
-        if (count <= kList) {
-            if (r.rank == 0) finish_list(r, p, sm, row, (int)count, top_k, top_p, min_mass);
+        uint64_t total, above;
+        double need = (double)top_k;
+        const int b = find_bin<false>(r, 0, 1.0f, need, total, above);
+        // (tokens below all bins are in the list too when the bins do not reach top_k)
+        const float t0 = b < kMassBins ? sm.t_max - (float)b : minus_inf();
+        const uint32_t n = make_list(r, sm, t0, sm.t_max, 0);
+        if (n <= kList) {
+            if (r.rank == 0) finish_list(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
             r.leave();
             return;
         }
         cut_count(r, sm, cut, top_k, p.vocab);
-        if (cut_p) {
+        if (top_p < 1.0f) {
             uint64_t z = 0, none;
             for (int i = r.tid; i < r.n; i += kSaThreads)
-                if (cut.in(r.keys[i], r.lo + i)) z += sm.mass(r.keys[i]);
-            const uint64_t total = r.sum(z, none);
+                if (cut.in(r.logits[i], r.lo + i)) z += sm.mass(r.logits[i]);
+            total = r.sum(z, none);
             cut_mass(r, sm, cut, fmax((double)top_p * (double)total, 1.0), p.vocab);
         }
-    } else if (cut_p) {
+    } else if (top_p < 1.0f) {
         // masses of all tokens; those below (1 - top_p) / vocab of the largest mass hold
         // less than 1 - top_p together, so the prefix ends above them
         const float tail = log2f((1.0f - top_p) / (float)p.vocab) - 0.5f;
-        const int last = tail > -31.0f ? (int)(-32.0f * tail) : kMassBins - 1;
-        uint64_t z = 0, none;
+        const float t_last = sm.t_max - fminf(fmaxf(floorf(-32.0f * tail), 0.0f), (float)(kMassBins - 1));
+        const float t_unit = sm.t_max - 46.0f * 32, t_none = sm.t_max - 32000.0f;
+        uint64_t z = 0;
         for (int i = r.tid * 4; i < r.n; i += kSaThreads * 4) {
-            const uint4 q = *reinterpret_cast<const uint4*>(r.keys + i);
-            const uint32_t key[4] = {q.x, q.y, q.z, q.w};
+            const float4 q = *reinterpret_cast<const float4*>(r.logits + i);
+            const float l[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                int k;
-                uint32_t M;
-                if (key[j] <= kNone || !sm.parts(key[j], k, M)) continue;
-                z += Softmax::fixed(k, M);
-                if (-k <= last && -k < kMassBins - 1) {
-                    atomicAdd(&hist[-k], M & 0xffffu);
-                    atomicAdd(&hist[kMassBins - k], M >> 16);
+                const float t = sm.place(l[j]);
+                if (!(t >= t_unit)) {
+                    z += t >= t_none ? 1 : 0;
+                    continue;
+                }
+                const uint32_t M = sm.mantissa(l[j], t);
+                const int bin = sm.bin(t);
+                z += max(Softmax::fixed(M, bin), (uint64_t)1);
+                if (t >= t_last) {
+                    atomicAdd(&r.hist[bin], M & 0xffffu);
+                    atomicAdd(&r.hist[kMassBins + bin], M >> 16);
                 }
             }
         }
-        const uint64_t total = r.sum(z, none);
-        const double need = fmax((double)top_p * (double)total, 1.0);
-        uint64_t above = 0;
-        const int b = find_bin<true>(r, need, above);
-        r.cl.sync();   // the histograms have been read: the scratch is free
+        uint64_t total = 0, above = 0;
+        double need = 0.0;
+        const int b = find_bin<true>(r, z, top_p, need, total, above);
         if (b >= kMassBins) {
             cut_mass(r, sm, cut, need, p.vocab);   // the prefix ends below the last bin
         } else {
             // every token has at most the largest mass: need / 2^45 tokens at least
+            const float t = sm.t_max - (float)b;
             if (need < (double)kList * (double)(1ull << kMassBits)) {
-                const uint32_t count = make_list(r, sm, 0, b);
-                if (count <= kList) {
-                    if (r.rank == 0) {
-                        if (r.tid == 0) r.sh->found_need = (uint64_t)__double_as_longlong(need);
-                        finish_list(r, p, sm, row, (int)count, 0, top_p, min_mass);
-                    }
+                const uint32_t n = make_list(r, sm, t, sm.t_max, 0);
+                if (n <= kList) {
+                    if (r.rank == 0) finish_list(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
                     r.leave();
                     return;
                 }
-                r.cl.sync();
-                if (writer) r.sh->list_count = 0;
-                r.cl.sync();
             }
-            const uint32_t count = make_list(r, sm, b, b);
-            if (count <= kList) {
+            const uint32_t n = make_list(r, sm, t, t, 1);
+            if (n <= kList) {
                 if (r.rank == 0) {
                     uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
-                    const uint64_t* list = sorted_list(r, (int)count);
-                    running_mass(r, sm, list, (int)count, above, run);
-                    const int n = prefix_reaching(r, run, (int)count, need);
+                    const uint64_t* list = sorted_list(r, (int)n);
+                    running_mass(r, sm, list, (int)n, above, run);
+                    const int last = prefix_reaching(r, run, (int)n, need) - 1;
                     if (r.tid < r.nb) {
                         SaShared* to = r.cl.map_shared_rank(r.sh, r.tid);
-                        to->cut_key = entry_key(list[n - 1]);
-                        to->cut_index = entry_index(list[n - 1]) + 1;
+                        to->cut_value = entry_logit(list[last]);
+                        to->cut_index = entry_index(list[last]) + 1;
                     }
                 }
                 r.cl.sync();
-                cut = Cut{r.sh->cut_key, r.sh->cut_index};
+                cut = Cut{r.sh->cut_value, r.sh->cut_index};
             } else {
                 cut_mass(r, sm, cut, need, p.vocab);
             }
         }
     }
+    if (min_logit > cut.K) cut = Cut{min_logit, p.vocab};
     // the kept mass, by warp (the tokens of a warp are neighbours), block and cluster
     const int w0 = r.warp * r.per_warp, w1 = min(r.n, w0 + r.per_warp);
     auto kept = [&](int i) -> uint64_t {
-        const uint32_t k = r.keys[i];
-        if (!cut.in(k, r.lo + i)) return 0;
-        const uint64_t m = sm.mass(k);
-        return (double)m < min_mass ? 0 : m;
+        const float l = r.logits[i];
+        return cut.in(l, r.lo + i) ? sm.mass(l) : 0;
     };
     uint64_t z = 0, before;
+#pragma unroll 2
     for (int i = w0 + r.lane; i < w1; i += 32) z += kept(i);
     const uint64_t mine = warp_sum_u64(z);
     const uint64_t total = r.sum(z, before);
@@ -748,7 +818,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
             const uint64_t inc = at + warp_scan_u64(m, r.lane);
             const uint32_t over = __ballot_sync(0xffffffffu, inc > target);
             if (over) {
-                if (r.lane == __ffs(over) - 1) choose(p, sm, row, r.lo + i, r.keys[i], total);
+                if (r.lane == __ffs(over) - 1) choose(p, sm, row, r.lo + i, r.logits[i], total);
                 break;
             }
             at = __shfl_sync(0xffffffffu, inc, 31);
@@ -765,12 +835,13 @@ cudaError_t launch_sample(const SampleParams& in, cudaStream_t s) {
     while (nb < kSaMaxCluster && p.vocab > nb * 8192) nb *= 2;
     const int unit = kSaWarps * 32;
     p.per_block = ((p.vocab + nb - 1) / nb + unit - 1) / unit * unit;
-    const size_t smem = (size_t)(kScratchWords + p.per_block) * 4;
+    constexpr int kFixed = kScratchWords + kHistWords;
+    const size_t smem = (size_t)(kFixed + p.per_block) * 4;
     const size_t esz = p.dtype == MOE_BF16 ? 2 : 4;
     const bool vec = ((uintptr_t)p.logits & 15) == 0 && (p.ld * (int64_t)esz) % 16 == 0;
     static std::atomic<uint64_t> attr[2];
     auto kern = vec ? sample_kernel<true> : sample_kernel<false>;
-    cudaError_t e = smem_attr_once(kern, (size_t)(kScratchWords + kSampleMaxVocab / kSaMaxCluster) * 4, attr[vec]);
+    cudaError_t e = smem_attr_once(kern, (size_t)(kFixed + kSampleMaxVocab / kSaMaxCluster) * 4, attr[vec]);
     if (e != cudaSuccess) return e;
     return launch_cluster(kern, dim3((unsigned)(p.rows * nb)), dim3(kSaThreads), nb, smem, s, p);
 }
