@@ -39,7 +39,6 @@ constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaMaxCluster = 8;
 constexpr int kMassBits = 45;
 constexpr int kList = 2048;               // tokens of a list
-constexpr int kShortList = 512;           // ranked by counting, else sorted
 constexpr int kMassBins = 1024;           // bins of 1/32 of a power of two
 constexpr int kKeyBins = 2048;            // bins of the selection by key bits
 // a block's scratch: a list of its own tokens and, in the first block, the row's
@@ -110,6 +109,12 @@ struct Softmax {
         if (!(t >= t_max - 46.0f * 32)) return t >= t_max - 32000.0f ? 1 : 0;
         return max(fixed(mantissa(l, t), bin(t)), (uint64_t)1);
     }
+    // the mass as a fraction of the largest, to 2^-21
+    __device__ __forceinline__ float approximate(float l) const {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(__fsub_rn(l, (float)m), c)));
+        return e;
+    }
     // the mass in 64 bits, for the chosen token's probability
     __device__ __forceinline__ double exact(float l) const { return exp2(((double)l - m) * cd); }
 };
@@ -134,6 +139,9 @@ struct SaShared {
     uint64_t coarse[32], total;           // this block's histogram by powers of two, and its mass
     uint64_t gather[2][kSaMaxCluster][32], gather_total[kSaMaxCluster];
     uint64_t found_above;
+    uint64_t block_above[kSaMaxCluster];  // in the first block: each block's mass over the bin of the cut
+    uint64_t pick_target, pick_total;
+    int32_t pick_block;
     uint32_t found;
     float cut_value;
     int32_t cut_index;
@@ -204,14 +212,15 @@ struct Row {
         __syncthreads();
         return warp_sum_u64(lane < kSaWarps ? sh->warp_sum[lane] : 0);
     }
-    // Inclusive scan of v over the threads of the block.
-    __device__ uint64_t block_scan(uint64_t v) {
+    // Inclusive scan of v over the threads of the block, and the sum of all.
+    __device__ uint64_t block_scan(uint64_t v, uint64_t& total) {
         v = warp_scan_u64(v, lane);
         __syncthreads();
         if (lane == 31) sh->warp_sum[warp] = v;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) v += sh->warp_sum[w];
-        return v;
+        uint64_t s = lane < kSaWarps ? sh->warp_sum[lane] : 0;
+        total = warp_sum_u64(s);
+        return v + warp_sum_u64(lane < warp ? s : 0);
     }
     // A block's last step: the others leave, the first one when none of them
     // reads its shared memory any more.
@@ -271,7 +280,8 @@ __device__ __noinline__ bool select_key(Row& r, const Softmax& sm, const Cut& cu
             mine += s;
         }
         if (r.tid == 0) r.sh->found = 0xffffffffu;
-        uint64_t before = above + r.block_scan(mine) - mine;
+        uint64_t all;
+        uint64_t before = above + r.block_scan(mine, all) - mine;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if ((double)before < need && (double)(before + v[j]) >= need) {
@@ -391,64 +401,62 @@ __device__ uint32_t make_list(Row& r, const Softmax& sm, float t0, float t1, int
     return *row_count;
 }
 
-// Sort n entries (a power of two), falling, by the threads of one block.
-__device__ void sort_falling(uint64_t* a, int n, int tid) {
+// Sort n entries (a power of two up to E x kSaThreads), falling: thread t holds
+// entries t, t + kSaThreads, ... of the order.  Bitonic; neighbours of a warp
+// exchange by shuffles, a thread's own entries in registers, the others through
+// `buf` (2 x E x kSaThreads words, used in turn).
+template <int E>
+__device__ void sort_falling(uint64_t (&v)[E], uint64_t* buf, int n, int tid) {
+    int turn = 0;
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
-            __syncthreads();
-            for (int t = tid; t < n / 2; t += kSaThreads) {
-                const int i = ((t & -step) << 1) | (t & (step - 1)), j = i + step;
-                const bool falling = (i & size) == 0;
-                const uint64_t x = a[i], y = a[j];
-                if ((x < y) == falling) {
-                    a[i] = y;
-                    a[j] = x;
-                }
+            if (E > 1 && step >= kSaThreads) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+#pragma unroll
+                    for (int d = 1; d < E; d <<= 1)
+                        if (step == d * kSaThreads && !(e & d)) {
+                            const bool falling = ((e * kSaThreads + tid) & size) == 0;
+                            const uint64_t x = v[e], y = v[(e | d) & (E - 1)];
+                            if ((x < y) == falling) {
+                                v[e] = y;
+                                v[(e | d) & (E - 1)] = x;
+                            }
+                        }
+                continue;
+            }
+            uint64_t* b = buf + turn * E * kSaThreads;
+            if (step >= 32) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) b[e * kSaThreads + tid] = v[e];
+                __syncthreads();
+                turn ^= 1;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = e * kSaThreads + tid;
+                const uint64_t x = v[e];
+                const uint64_t y = step >= 32 ? b[i ^ step] : __shfl_xor_sync(0xffffffffu, x, step);
+                const bool larger = ((i & size) == 0) == ((i & step) == 0);   // this place keeps the larger one
+                v[e] = (x > y) == larger ? x : y;
             }
         }
-    __syncthreads();
 }
 
 __device__ int pow2_at_least(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
 
-// Sort the row's list of `count` entries; the first block only.
-__device__ uint64_t* sorted_list(Row& r, int count) {
-    uint64_t* list = reinterpret_cast<uint64_t*>(r.scratch) + kList;
-    const int n = pow2_at_least(count);
-    for (int i = count + r.tid; i < n; i += kSaThreads) list[i] = 0;
-    sort_falling(list, n, r.tid);
-    return list;
-}
-
-// Of the list's first `count` entries, in order: the running mass (plus
-// `above`) after entry i to run[i].  The first block only.
-__device__ void running_mass(Row& r, const Softmax& sm, const uint64_t* list, int count, uint64_t above, uint64_t* run) {
-    constexpr int kPer = kList / kSaThreads;
-    uint64_t v[kPer], mine = 0;
+// The running masses of entries held as sort_falling leaves them, after each
+// one, and their sum.
+template <int E>
+__device__ uint64_t running_mass(Row& r, const uint64_t (&mass)[E], uint64_t (&run)[E]) {
+    uint64_t at = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int i = r.tid * kPer + j;
-        v[j] = i < count ? sm.mass(entry_logit(list[i])) : 0;
-        mine += v[j];
+    for (int e = 0; e < E; ++e) {
+        uint64_t total;
+        run[e] = at + r.block_scan(mass[e], total);
+        at += total;
     }
-    uint64_t at = above + r.block_scan(mine) - mine;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        at += v[j];
-        if (r.tid * kPer + j < count) run[r.tid * kPer + j] = at;
-    }
-    __syncthreads();
-}
-
-// Number of entries whose running mass, without themselves, is below `need`
-// (at least one).  The first block only.
-__device__ int prefix_reaching(Row& r, const uint64_t* run, int count, double need) {
-    if (r.tid == 0) r.sh->found = count;
-    __syncthreads();
-    for (int i = r.tid; i < count; i += kSaThreads)
-        if ((double)run[i] >= need) atomicMin(&r.sh->found, (uint32_t)(i + 1));
-    __syncthreads();
-    return (int)r.sh->found;
+    return at;
 }
 
 __device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
@@ -464,79 +472,96 @@ __device__ void choose(const SampleParams& p, const Softmax& sm, int row, int in
 // Finish a row whose tokens in the running are all in the list, by the first
 // block alone.  top_p < 1: the prefix reaches `need`, or (top_k > 0) top_p of
 // the mass of the first top_k.
+template <int E>
 __device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int count, int top_k, float top_p,
                             double need, float min_logit) {
-    uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
-    if (count <= kShortList) {
-        // by counting: `parts` neighbouring threads per entry add up what precedes it
-        uint64_t* list = run + kList;
-        const int parts = kSaThreads / max(pow2_at_least(count), 16);
-        const int i = r.tid / parts, part = r.tid % parts;
-        const uint64_t mine = i < count ? list[i] : 0;
-        const uint64_t mass = i < count ? sm.mass(entry_logit(mine)) : 0;
-        if (part == 0 && i < count) run[i] = mass;
-        __syncthreads();
-        uint64_t before = 0;
-        int rank = 0;
-        if (i < count)
-            for (int j = part; j < count; j += parts)
-                if (list[j] > mine) {
-                    ++rank;
-                    before += run[j];
-                }
-        for (int o = parts >> 1; o >= 1; o >>= 1) {
-            rank += __shfl_xor_sync(0xffffffffu, rank, o);
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-        }
-        const bool own = part == 0 && i < count;
-        bool in = own && (top_k <= 0 || rank < top_k);
-        if (top_p < 1.0f) {
-            if (top_k > 0) need = fmax((double)top_p * (double)r.block_sum(in ? mass : 0), 1.0);
-            in = in && (rank == 0 || (double)before < need);
-        }
-        in = in && (rank == 0 || entry_logit(mine) >= min_logit);
-        const uint64_t total = r.block_sum(in ? mass : 0);   // (its barriers end the reads of run)
-        if (own) run[i] = in ? mass : 0;
-        const uint64_t target = target_of(p.u[row], total);
-        __syncthreads();
-        // in the order of the tokens: ~index falls as the index rises
-        uint64_t sum = 0;
-        if (i < count)
-            for (int j = part; j < count; j += parts)
-                if ((uint32_t)list[j] > (uint32_t)mine) sum += run[j];
-        for (int o = parts >> 1; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (in && sum <= target && target < sum + mass) choose(p, sm, row, entry_index(mine), entry_logit(mine), total);
-        return;
+    uint64_t* buf = reinterpret_cast<uint64_t*>(r.scratch);
+    uint64_t v[E], mass[E], run[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        v[e] = i < count ? buf[kList + i] : 0;
     }
-    uint64_t* list = sorted_list(r, count);
-    int n = top_k > 0 ? min(count, top_k) : count;
-    running_mass(r, sm, list, n, 0, run);
-    if (top_p < 1.0f) {
-        if (top_k > 0) need = fmax((double)top_p * (double)run[n - 1], 1.0);
-        n = prefix_reaching(r, run, n, need);
+    __syncthreads();   // the list is in registers: its place serves the sort
+    sort_falling<E>(v, buf, pow2_at_least(count), r.tid);
+    const int first = top_k > 0 ? min(count, top_k) : count;
+#pragma unroll
+    for (int e = 0; e < E; ++e) mass[e] = e * kSaThreads + r.tid < first ? sm.mass(entry_logit(v[e])) : 0;
+    const uint64_t z = running_mass<E>(r, mass, run);
+    if (top_k > 0) need = fmax((double)top_p * (double)z, 1.0);
+    uint64_t kept = 0;
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        const bool in = i < first && (i == 0 || ((top_p >= 1.0f || (double)(run[e] - mass[e]) < need) &&
+                                                 entry_logit(v[e]) >= min_logit));
+        kept += in ? mass[e] : 0;
+        n += in;
+        v[e] = in ? (v[e] << 32) | (v[e] >> 32) : 0;   // ~index on top: it falls as the index rises
     }
-    if (r.tid == 0) r.sh->found = n;
-    __syncthreads();
-    for (int i = r.tid; i < n; i += kSaThreads)
-        if (entry_logit(list[i]) < min_logit) atomicMin(&r.sh->found, (uint32_t)i);
-    __syncthreads();
-    n = max(1, (int)r.sh->found);
-    const uint64_t total = run[n - 1];
+    const uint64_t total = r.block_sum(kept);
+    n = (int)r.block_sum((uint64_t)n);
     const uint64_t target = target_of(p.u[row], total);
-    // in the order of the tokens: entries with ~index on top, sorted again
-    __syncthreads();
-    const int m = pow2_at_least(n);
-    for (int i = r.tid; i < m; i += kSaThreads) {
-        const uint64_t e = list[i];
-        list[i] = i < n ? (e << 32) | (e >> 32) : 0;
+    sort_falling<E>(v, buf, pow2_at_least(n), r.tid);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        v[e] = (v[e] << 32) | (v[e] >> 32);
+        mass[e] = v[e] ? sm.mass(entry_logit(v[e])) : 0;
     }
-    sort_falling(list, m, r.tid);
-    for (int i = r.tid; i < n; i += kSaThreads) list[i] = (list[i] << 32) | (list[i] >> 32);
+    running_mass<E>(r, mass, run);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (target < run[e] && run[e] - mass[e] <= target) choose(p, sm, row, entry_index(v[e]), entry_logit(v[e]), total);
+}
+
+// Of a list of tokens of one bin, `above` being the mass over it (block_above:
+// each block's): the last one of the prefix that reaches `need`, and, if no other
+// cut follows, the block that holds the token to choose and what is left of the
+// target there.  Written to every block of the cluster.
+template <int E>
+__device__ void cut_in_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int count, uint64_t above, double need) {
+    uint64_t* buf = reinterpret_cast<uint64_t*>(r.scratch);
+    uint64_t v[E], mass[E], run[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        v[e] = i < count ? buf[kList + i] : 0;
+    }
     __syncthreads();
-    running_mass(r, sm, list, n, 0, run);
-    for (int i = r.tid; i < n; i += kSaThreads)
-        if (run[i] > target && (i == 0 || run[i - 1] <= target))
-            choose(p, sm, row, entry_index(list[i]), entry_logit(list[i]), total);
+    sort_falling<E>(v, buf, pow2_at_least(count), r.tid);
+#pragma unroll
+    for (int e = 0; e < E; ++e) mass[e] = e * kSaThreads + r.tid < count ? sm.mass(entry_logit(v[e])) : 0;
+    running_mass<E>(r, mass, run);
+    uint64_t kept = 0;
+    SaShared* sh = r.sh;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        const bool in = i < count && (i == 0 || (double)(above + run[e] - mass[e]) < need);
+        kept += in ? mass[e] : 0;
+        // the last one of the prefix: the next would not be in it
+        const bool last = in && (i + 1 == count || (double)(above + run[e]) >= need);
+        if (last) {
+            sh->cut_value = entry_logit(v[e]);
+            sh->cut_index = entry_index(v[e]) + 1;
+        }
+        if (in) atomicAdd((unsigned long long*)&sh->block_above[entry_index(v[e]) / p.per_block], (unsigned long long)mass[e]);
+    }
+    const uint64_t total = above + r.block_sum(kept);
+    __syncthreads();
+    const uint64_t target = target_of(p.u[row], total);
+    if (r.tid < r.nb) {
+        uint64_t before = 0;
+        int b = 0;
+        while (b + 1 < r.nb && before + sh->block_above[b] <= target) before += sh->block_above[b++];
+        SaShared* to = r.cl.map_shared_rank(sh, r.tid);
+        to->cut_value = sh->cut_value;
+        to->cut_index = sh->cut_index;
+        to->pick_block = b;
+        to->pick_target = target - before;
+        to->pick_total = total;
+    }
 }
 
 // ------------------------------------------------------------------ the histogram
@@ -591,11 +616,51 @@ __device__ int find_bin(Row& r, uint64_t own, float top_p, double& need, uint64_
     at = __ballot_sync(0xffffffffu, (double)inc >= need);
     const int j = __ffs(at) - 1;   // the bins of g add up to its sum: one is found
     above = __shfl_sync(0xffffffffu, inc - s, j);
+    if (MASS && r.warp < r.nb) {
+        const uint64_t own_above = warp_sum_u64((r.lane < g ? r.sh->gather[0][r.warp][r.lane] : 0) +
+                                                (r.lane < j ? r.sh->gather[1][r.warp][r.lane] : 0));
+        if (r.lane == 0) r.sh->block_above[r.warp] = own_above;
+    }
     return g * 32 + j;
 }
 
 __device__ __forceinline__ float clean(float v, bool allowed) {
     return allowed && v == v ? __fadd_rn(v, 0.0f) : minus_inf();
+}
+
+__device__ __forceinline__ uint64_t kept_mass(const Row& r, const Softmax& sm, const Cut& cut, int i) {
+    const float l = r.logits[i];
+    return cut.in(l, r.lo + i) ? sm.mass(l) : 0;
+}
+
+// The token of this block at which the running mass of those inside `cut`, in
+// their order, exceeds `target` (the last one, should a sum of rounded masses
+// fall short of it).
+__device__ void pick_in_block(Row& r, const SampleParams& p, const Softmax& sm, int row, const Cut& cut, uint64_t target,
+                              uint64_t total) {
+    const int w0 = r.warp * r.per_warp, w1 = min(r.n, w0 + r.per_warp);
+    uint64_t z = 0;
+#pragma unroll 2
+    for (int i = w0 + r.lane; i < w1; i += 32) z += kept_mass(r, sm, cut, i);
+    z = warp_sum_u64(z);
+    __syncthreads();
+    if (r.lane == 0) r.sh->warp_sum[r.warp] = z;
+    __syncthreads();
+    const uint64_t s = r.lane < kSaWarps ? r.sh->warp_sum[r.lane] : 0;
+    const uint64_t block = warp_sum_u64(s);
+    uint64_t at = warp_sum_u64(r.lane < r.warp ? s : 0);
+    target = min(target, block - 1);
+    if (at > target || target >= at + z) return;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + r.lane;
+        const uint64_t inc = at + warp_scan_u64(i < w1 ? kept_mass(r, sm, cut, i) : 0, r.lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, inc > target);
+        if (over) {
+            if (r.lane == __ffs(over) - 1) choose(p, sm, row, r.lo + i, r.logits[i], total);
+            return;
+        }
+        at = __shfl_sync(0xffffffffu, inc, 31);
+    }
 }
 
 template <bool VEC>
@@ -664,7 +729,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
     }
     const float temp = p.temperature ? fminf(p.temperature[row], 3e38f) : 1.0f;
     const int top_k = p.top_k ? p.top_k[row] : 0;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f;
+    const float top_p = p.top_p && p.top_p[row] < 1.0f ? p.top_p[row] : 1.0f;   // (a NaN is off)
     const float min_p = p.min_p ? p.min_p[row] : 0.0f;
     float top = r.max_logit(own_max);
     const bool writer = r.rank == 0 && r.tid == 0;
@@ -719,7 +784,12 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         const float t0 = b < kMassBins ? sm.t_max - (float)b : minus_inf();
         const uint32_t n = make_list(r, sm, t0, sm.t_max, 0);
         if (n <= kList) {
-            if (r.rank == 0) finish_list(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
+            if (r.rank == 0) {
+                if (n <= kSaThreads)
+                    finish_list<1>(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
+                else
+                    finish_list<kList / kSaThreads>(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
+            }
             r.leave();
             return;
         }
@@ -732,31 +802,30 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
             cut_mass(r, sm, cut, fmax((double)top_p * (double)total, 1.0), p.vocab);
         }
     } else if (top_p < 1.0f) {
-        // masses of all tokens; those below (1 - top_p) / vocab of the largest mass hold
-        // less than 1 - top_p together, so the prefix ends above them
-        const float tail = log2f((1.0f - top_p) / (float)p.vocab) - 0.5f;
+        // masses of all tokens; those below tail / vocab of the largest mass hold less than
+        // tail <= 1 - top_p together, so the prefix ends above them
+        const float tail = log2f(fminf(1.0f - top_p, 0.015625f) / (float)p.vocab) - 0.5f;
         const float t_last = sm.t_max - fminf(fmaxf(floorf(-32.0f * tail), 0.0f), (float)(kMassBins - 1));
-        const float t_unit = sm.t_max - 46.0f * 32, t_none = sm.t_max - 32000.0f;
         uint64_t z = 0;
+        float zt = 0.0f;   // the tail's part, less than 1/64 in all, by the approximate 2^x
         for (int i = r.tid * 4; i < r.n; i += kSaThreads * 4) {
             const float4 q = *reinterpret_cast<const float4*>(r.logits + i);
             const float l[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float t = sm.place(l[j]);
-                if (!(t >= t_unit)) {
-                    z += t >= t_none ? 1 : 0;
-                    continue;
-                }
-                const uint32_t M = sm.mantissa(l[j], t);
-                const int bin = sm.bin(t);
-                z += max(Softmax::fixed(M, bin), (uint64_t)1);
                 if (t >= t_last) {
+                    const uint32_t M = sm.mantissa(l[j], t);
+                    const int bin = sm.bin(t);
+                    z += max(Softmax::fixed(M, bin), (uint64_t)1);
                     atomicAdd(&r.hist[bin], M & 0xffffu);
                     atomicAdd(&r.hist[kMassBins + bin], M >> 16);
+                } else {
+                    zt += sm.approximate(l[j]);
                 }
             }
         }
+        z += (uint64_t)((double)zt * (double)(1ull << kMassBits));
         uint64_t total = 0, above = 0;
         double need = 0.0;
         const int b = find_bin<true>(r, z, top_p, need, total, above);
@@ -768,7 +837,12 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
             if (need < (double)kList * (double)(1ull << kMassBits)) {
                 const uint32_t n = make_list(r, sm, t, sm.t_max, 0);
                 if (n <= kList) {
-                    if (r.rank == 0) finish_list(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
+                    if (r.rank == 0) {
+                        if (n <= kSaThreads)
+                            finish_list<1>(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
+                        else
+                            finish_list<kList / kSaThreads>(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
+                    }
                     r.leave();
                     return;
                 }
@@ -776,54 +850,32 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
             const uint32_t n = make_list(r, sm, t, t, 1);
             if (n <= kList) {
                 if (r.rank == 0) {
-                    uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
-                    const uint64_t* list = sorted_list(r, (int)n);
-                    running_mass(r, sm, list, (int)n, above, run);
-                    const int last = prefix_reaching(r, run, (int)n, need) - 1;
-                    if (r.tid < r.nb) {
-                        SaShared* to = r.cl.map_shared_rank(r.sh, r.tid);
-                        to->cut_value = entry_logit(list[last]);
-                        to->cut_index = entry_index(list[last]) + 1;
-                    }
+                    if (n <= kSaThreads)
+                        cut_in_list<1>(r, p, sm, row, (int)n, above, need);
+                    else
+                        cut_in_list<kList / kSaThreads>(r, p, sm, row, (int)n, above, need);
                 }
                 r.cl.sync();
                 cut = Cut{r.sh->cut_value, r.sh->cut_index};
+                if (!(min_logit > cut.K)) {
+                    // the histograms tell which block holds the token: the others are done
+                    if (r.rank == r.sh->pick_block) pick_in_block(r, p, sm, row, cut, r.sh->pick_target, r.sh->pick_total);
+                    return;
+                }
             } else {
                 cut_mass(r, sm, cut, need, p.vocab);
             }
         }
     }
     if (min_logit > cut.K) cut = Cut{min_logit, p.vocab};
-    // the kept mass, by warp (the tokens of a warp are neighbours), block and cluster
-    const int w0 = r.warp * r.per_warp, w1 = min(r.n, w0 + r.per_warp);
-    auto kept = [&](int i) -> uint64_t {
-        const float l = r.logits[i];
-        return cut.in(l, r.lo + i) ? sm.mass(l) : 0;
-    };
+    // the kept mass, by block and cluster
     uint64_t z = 0, before;
 #pragma unroll 2
-    for (int i = w0 + r.lane; i < w1; i += 32) z += kept(i);
-    const uint64_t mine = warp_sum_u64(z);
+    for (int i = r.tid; i < r.n; i += kSaThreads) z += kept_mass(r, sm, cut, i);
+    const uint64_t mine = r.block_sum(z);
     const uint64_t total = r.sum(z, before);
     const uint64_t target = target_of(p.u[row], total);
-    __syncthreads();
-    if (r.lane == 0) r.sh->warp_sum[r.warp] = mine;
-    __syncthreads();
-    for (int w = 0; w < r.warp; ++w) before += r.sh->warp_sum[w];
-    if (before <= target && target < before + mine) {
-        uint64_t at = before;
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const int i = i0 + r.lane;
-            const uint64_t m = i < w1 ? kept(i) : 0;
-            const uint64_t inc = at + warp_scan_u64(m, r.lane);
-            const uint32_t over = __ballot_sync(0xffffffffu, inc > target);
-            if (over) {
-                if (r.lane == __ffs(over) - 1) choose(p, sm, row, r.lo + i, r.logits[i], total);
-                break;
-            }
-            at = __shfl_sync(0xffffffffu, inc, 31);
-        }
-    }
+    if (before <= target && target < before + mine) pick_in_block(r, p, sm, row, cut, target - before, total);
     r.cl.sync();   // no block leaves while another may still write to its slots
 }
 
