@@ -401,6 +401,8 @@ __device__ uint32_t make_list(Row& r, const Softmax& sm, float t0, float t1, int
     return *row_count;
 }
 
+__device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
+
 // Sort n entries (a power of two up to E x kSaThreads), falling: thread t holds
 // entries t, t + kSaThreads, ... of the order.  Bitonic; neighbours of a warp
 // exchange by shuffles, a thread's own entries in registers, the others through
@@ -443,20 +445,105 @@ __device__ void sort_falling(uint64_t (&v)[E], uint64_t* buf, int n, int tid) {
         }
 }
 
-__device__ int pow2_at_least(int n) { return n <= 2 ? 2 : 1 << (32 - __clz(n - 1)); }
-
-// The running masses of entries held as sort_falling leaves them, after each
-// one, and their sum.
-template <int E>
-__device__ uint64_t running_mass(Row& r, const uint64_t (&mass)[E], uint64_t (&run)[E]) {
-    uint64_t at = 0;
+// Bring n entries (list[0 .. n), in any order) into falling order of the
+// entries, or of the entries with their halves exchanged (rising index), with
+// run[i] the mass up to and with entry i.  By one block; list and run are the two
+// halves of its scratch.
+template <int E, bool BY_INDEX>
+__device__ void order_by_sort(Row& r, const Softmax& sm, uint64_t* list, uint64_t* run, int n) {
+    uint64_t v[E], at = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        v[e] = i < n ? list[i] : 0;
+        if (BY_INDEX) v[e] = (v[e] << 32) | (v[e] >> 32);
+    }
+    __syncthreads();   // the list is in registers: its place serves the sort
+    sort_falling<E>(v, run, pow2_at_least(n), r.tid);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = e * kSaThreads + r.tid;
+        if (BY_INDEX) v[e] = (v[e] << 32) | (v[e] >> 32);
         uint64_t total;
-        run[e] = at + r.block_scan(mass[e], total);
+        const uint64_t inc = r.block_scan(i < n ? sm.mass(entry_logit(v[e])) : 0, total);
+        if (i < n) {
+            list[i] = v[e];
+            run[i] = at + inc;
+        }
         at += total;
     }
-    return at;
+    __syncthreads();
+}
+
+// The same for at most kCounted entries, by counting: `parts` neighbouring
+// threads per entry add up what precedes it.  (The sort's 28 steps for 128
+// entries took 3 us.)
+constexpr int kCounted = 128;
+
+template <bool BY_INDEX>
+__device__ __noinline__ void order_by_count(Row& r, const Softmax& sm, uint64_t* list, uint64_t* run, int n) {
+    uint64_t* order = run + 512;      // what the entries are ordered by, and their masses
+    uint64_t* mass = run + 1024;
+    const int parts = min(32, kSaThreads / pow2_at_least(n));
+    const int i = r.tid / parts, part = r.tid % parts;
+    uint64_t e = 0, mine = 0, m = 0;
+    if (i < n) {
+        e = list[i];
+        mine = BY_INDEX ? (e << 32) | (e >> 32) : e;
+        m = sm.mass(entry_logit(e));
+        if (part == 0) {
+            order[i] = mine;
+            mass[i] = m;
+        }
+    }
+    __syncthreads();
+    uint64_t before = 0;
+    int place = 0;
+    if (i < n) {
+#pragma unroll 4
+        for (int j = part; j < n; j += parts) {
+            const bool over = order[j] > mine;
+            before += over ? mass[j] : 0;
+            place += over;
+        }
+    }
+    for (int o = parts >> 1; o >= 1; o >>= 1) {
+        place += __shfl_xor_sync(0xffffffffu, place, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (i < n && part == 0) {         // every entry of the list has been read
+        list[place] = e;
+        run[place] = before + m;
+    }
+    __syncthreads();
+}
+
+template <bool BY_INDEX>
+__device__ __forceinline__ void order_list(Row& r, const Softmax& sm, uint64_t* list, uint64_t* run, int n) {
+    if (n <= kCounted)
+        order_by_count<BY_INDEX>(r, sm, list, run, n);
+    else if (n <= kSaThreads)
+        order_by_sort<1, BY_INDEX>(r, sm, list, run, n);
+    else
+        order_by_sort<kList / kSaThreads, BY_INDEX>(r, sm, list, run, n);
+}
+
+// The first of n places where `at` holds (it holds from there on), by one warp;
+// n if there is none.
+template <class Pred>
+__device__ __forceinline__ int first_where(int n, int lane, Pred at) {
+    int lo = 0, len = n;
+    while (len > 0) {
+        const int step = (len + 31) / 32, i = min(len, (lane + 1) * step) - 1;
+        const uint32_t b = __ballot_sync(0xffffffffu, at(lo + i));
+        if (!b) return lo + len;
+        const int f = __ffs(b) - 1;
+        if (step == 1) return lo + f;
+        len = min(step, len - f * step) - 1;   // its last place holds: among the others, or that one
+        lo += f * step;
+    }
+    return lo;
 }
 
 __device__ __forceinline__ uint64_t target_of(float u, uint64_t total) {
@@ -469,95 +556,53 @@ __device__ void choose(const SampleParams& p, const Softmax& sm, int row, int in
     if (p.prob) p.prob[row] = (float)(sm.exact(l) * (double)(1ull << kMassBits) / (double)total);
 }
 
-// Finish a row whose tokens in the running are all in the list, by the first
-// block alone.  top_p < 1: the prefix reaches `need`, or (top_k > 0) top_p of
-// the mass of the first top_k.
-template <int E>
-__device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int count, int top_k, float top_p,
+// Finish a row whose n tokens in the running are all in the list, by the first
+// block alone; every warp follows the steps that are not the whole block's.
+// top_p < 1: the prefix reaches `need`, or (top_k > 0) top_p of the mass of the
+// first top_k.
+__device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int n, int top_k, float top_p,
                             double need, float min_logit) {
-    uint64_t* buf = reinterpret_cast<uint64_t*>(r.scratch);
-    uint64_t v[E], mass[E], run[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        v[e] = i < count ? buf[kList + i] : 0;
+    uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
+    uint64_t* list = run + kList;
+    order_list<false>(r, sm, list, run, n);
+    if (top_k > 0) n = min(n, top_k);
+    if (top_p < 1.0f) {
+        if (top_k > 0) need = fmax((double)top_p * (double)run[n - 1], 1.0);
+        n = min(n, first_where(n, r.lane, [&](int i) { return (double)run[i] >= need; }) + 1);
     }
-    __syncthreads();   // the list is in registers: its place serves the sort
-    sort_falling<E>(v, buf, pow2_at_least(count), r.tid);
-    const int first = top_k > 0 ? min(count, top_k) : count;
-#pragma unroll
-    for (int e = 0; e < E; ++e) mass[e] = e * kSaThreads + r.tid < first ? sm.mass(entry_logit(v[e])) : 0;
-    const uint64_t z = running_mass<E>(r, mass, run);
-    if (top_k > 0) need = fmax((double)top_p * (double)z, 1.0);
-    uint64_t kept = 0;
-    int n = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        const bool in = i < first && (i == 0 || ((top_p >= 1.0f || (double)(run[e] - mass[e]) < need) &&
-                                                 entry_logit(v[e]) >= min_logit));
-        kept += in ? mass[e] : 0;
-        n += in;
-        v[e] = in ? (v[e] << 32) | (v[e] >> 32) : 0;   // ~index on top: it falls as the index rises
-    }
-    const uint64_t total = r.block_sum(kept);
-    n = (int)r.block_sum((uint64_t)n);
+    n = max(1, first_where(n, r.lane, [&](int i) { return entry_logit(list[i]) < min_logit; }));
+    const uint64_t total = run[n - 1];
     const uint64_t target = target_of(p.u[row], total);
-    sort_falling<E>(v, buf, pow2_at_least(n), r.tid);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        v[e] = (v[e] << 32) | (v[e] >> 32);
-        mass[e] = v[e] ? sm.mass(entry_logit(v[e])) : 0;
+    __syncthreads();
+    order_list<true>(r, sm, list, run, n);
+    if (r.warp == 0) {
+        const int at = first_where(n, r.lane, [&](int i) { return run[i] > target; });
+        if (r.lane == 0) choose(p, sm, row, entry_index(list[at]), entry_logit(list[at]), total);
     }
-    running_mass<E>(r, mass, run);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (target < run[e] && run[e] - mass[e] <= target) choose(p, sm, row, entry_index(v[e]), entry_logit(v[e]), total);
 }
 
-// Of a list of tokens of one bin, `above` being the mass over it (block_above:
+// Of a list of n tokens of one bin, `above` being the mass over it (block_above:
 // each block's): the last one of the prefix that reaches `need`, and, if no other
 // cut follows, the block that holds the token to choose and what is left of the
 // target there.  Written to every block of the cluster.
-template <int E>
-__device__ void cut_in_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int count, uint64_t above, double need) {
-    uint64_t* buf = reinterpret_cast<uint64_t*>(r.scratch);
-    uint64_t v[E], mass[E], run[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        v[e] = i < count ? buf[kList + i] : 0;
-    }
-    __syncthreads();
-    sort_falling<E>(v, buf, pow2_at_least(count), r.tid);
-#pragma unroll
-    for (int e = 0; e < E; ++e) mass[e] = e * kSaThreads + r.tid < count ? sm.mass(entry_logit(v[e])) : 0;
-    running_mass<E>(r, mass, run);
-    uint64_t kept = 0;
-    SaShared* sh = r.sh;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        const bool in = i < count && (i == 0 || (double)(above + run[e] - mass[e]) < need);
-        kept += in ? mass[e] : 0;
-        // the last one of the prefix: the next would not be in it
-        const bool last = in && (i + 1 == count || (double)(above + run[e]) >= need);
-        if (last) {
-            sh->cut_value = entry_logit(v[e]);
-            sh->cut_index = entry_index(v[e]) + 1;
-        }
-        if (in) atomicAdd((unsigned long long*)&sh->block_above[entry_index(v[e]) / p.per_block], (unsigned long long)mass[e]);
-    }
-    const uint64_t total = above + r.block_sum(kept);
-    __syncthreads();
+__device__ void cut_in_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int n, uint64_t above, double need) {
+    uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
+    uint64_t* list = run + kList;
+    order_list<false>(r, sm, list, run, n);
+    const int last = min(n - 1, first_where(n, r.lane, [&](int i) { return (double)(above + run[i]) >= need; }));
+    for (int i = r.tid; i <= last; i += kSaThreads)
+        atomicAdd((unsigned long long*)&r.sh->block_above[entry_index(list[i]) / p.per_block],
+                  (unsigned long long)(run[i] - (i ? run[i - 1] : 0)));
+    const uint64_t total = above + run[last];
     const uint64_t target = target_of(p.u[row], total);
+    __syncthreads();
     if (r.tid < r.nb) {
         uint64_t before = 0;
         int b = 0;
-        while (b + 1 < r.nb && before + sh->block_above[b] <= target) before += sh->block_above[b++];
-        SaShared* to = r.cl.map_shared_rank(sh, r.tid);
-        to->cut_value = sh->cut_value;
-        to->cut_index = sh->cut_index;
+        while (b + 1 < r.nb && before + r.sh->block_above[b] <= target) before += r.sh->block_above[b++];
+        SaShared* to = r.cl.map_shared_rank(r.sh, r.tid);
+        to->cut_value = entry_logit(list[last]);
+        to->cut_index = entry_index(list[last]) + 1;
         to->pick_block = b;
         to->pick_target = target - before;
         to->pick_total = total;
@@ -638,28 +683,36 @@ __device__ __forceinline__ uint64_t kept_mass(const Row& r, const Softmax& sm, c
 // fall short of it).
 __device__ void pick_in_block(Row& r, const SampleParams& p, const Softmax& sm, int row, const Cut& cut, uint64_t target,
                               uint64_t total) {
-    const int w0 = r.warp * r.per_warp, w1 = min(r.n, w0 + r.per_warp);
+    // a lane owns `run` neighbouring tokens, read in turn from a place of its own so
+    // that the lanes' reads fall into different banks
+    const int run = r.per_warp / 32, l0 = (r.warp * 32 + r.lane) * run;
     uint64_t z = 0;
 #pragma unroll 2
-    for (int i = w0 + r.lane; i < w1; i += 32) z += kept_mass(r, sm, cut, i);
-    z = warp_sum_u64(z);
+    for (int j = 0; j < run; ++j) {
+        int o = j + r.lane;
+        o -= o >= run ? o / run * run : 0;
+        if (l0 + o < r.n) z += kept_mass(r, sm, cut, l0 + o);
+    }
+    const uint64_t inc = warp_scan_u64(z, r.lane);
     __syncthreads();
-    if (r.lane == 0) r.sh->warp_sum[r.warp] = z;
+    if (r.lane == 31) r.sh->warp_sum[r.warp] = inc;
     __syncthreads();
     const uint64_t s = r.lane < kSaWarps ? r.sh->warp_sum[r.lane] : 0;
-    const uint64_t block = warp_sum_u64(s);
-    uint64_t at = warp_sum_u64(r.lane < r.warp ? s : 0);
-    target = min(target, block - 1);
-    if (at > target || target >= at + z) return;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + r.lane;
-        const uint64_t inc = at + warp_scan_u64(i < w1 ? kept_mass(r, sm, cut, i) : 0, r.lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, inc > target);
+    target = min(target, warp_sum_u64(s) - 1);
+    const uint64_t at = warp_sum_u64(r.lane < r.warp ? s : 0);
+    const uint32_t holds = __ballot_sync(0xffffffffu, at + inc - z <= target && target < at + inc);
+    if (!holds) return;
+    const int owner = __ffs(holds) - 1;
+    uint64_t before = at + __shfl_sync(0xffffffffu, inc - z, owner);
+    for (int j0 = 0; j0 < run; j0 += 32) {
+        const int i = (r.warp * 32 + owner) * run + j0 + r.lane;
+        const uint64_t m = warp_scan_u64(j0 + r.lane < run && i < r.n ? kept_mass(r, sm, cut, i) : 0, r.lane);
+        const uint32_t over = __ballot_sync(0xffffffffu, before + m > target);
         if (over) {
             if (r.lane == __ffs(over) - 1) choose(p, sm, row, r.lo + i, r.logits[i], total);
             return;
         }
-        at = __shfl_sync(0xffffffffu, inc, 31);
+        before += __shfl_sync(0xffffffffu, m, 31);
     }
 }
 
@@ -784,12 +837,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         const float t0 = b < kMassBins ? sm.t_max - (float)b : minus_inf();
         const uint32_t n = make_list(r, sm, t0, sm.t_max, 0);
         if (n <= kList) {
-            if (r.rank == 0) {
-                if (n <= kSaThreads)
-                    finish_list<1>(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
-                else
-                    finish_list<kList / kSaThreads>(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
-            }
+            if (r.rank == 0) finish_list(r, p, sm, row, (int)n, top_k, top_p, 0.0, min_logit);
             r.leave();
             return;
         }
@@ -837,24 +885,14 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
             if (need < (double)kList * (double)(1ull << kMassBits)) {
                 const uint32_t n = make_list(r, sm, t, sm.t_max, 0);
                 if (n <= kList) {
-                    if (r.rank == 0) {
-                        if (n <= kSaThreads)
-                            finish_list<1>(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
-                        else
-                            finish_list<kList / kSaThreads>(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
-                    }
+                    if (r.rank == 0) finish_list(r, p, sm, row, (int)n, 0, top_p, need, min_logit);
                     r.leave();
                     return;
                 }
             }
             const uint32_t n = make_list(r, sm, t, t, 1);
             if (n <= kList) {
-                if (r.rank == 0) {
-                    if (n <= kSaThreads)
-                        cut_in_list<1>(r, p, sm, row, (int)n, above, need);
-                    else
-                        cut_in_list<kList / kSaThreads>(r, p, sm, row, (int)n, above, need);
-                }
+                if (r.rank == 0) cut_in_list(r, p, sm, row, (int)n, above, need);
                 r.cl.sync();
                 cut = Cut{r.sh->cut_value, r.sh->cut_index};
                 if (!(min_logit > cut.K)) {
