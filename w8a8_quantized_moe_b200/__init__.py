@@ -197,9 +197,15 @@ def lib():
 
 # ------------------------------------------------------------------ marshalling helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t, dtype=None, name="tensor", allow_none=False):
@@ -256,8 +262,8 @@ def _host_ptr(a, name="array", allow_none=False):
 
 def _stream(stream):
     if stream is None:
-        torch = _torch()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -633,20 +639,20 @@ def moe_w8a8_ep_combine_blocked(w: Weights, o_blocks, T: int, rank_first, block_
 
 # ------------------------------------------------------------------ around the layer
 
-def _cuda(t, name, dtypes, dev):
-    """A CUDA tensor of one of the types on the current device."""
+def _refuse(t, name, dtype, dev):
+    """Why a tensor is not a CUDA tensor of the type on the current device."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on device {t.get_device()}, the current one is {dev}")
 
 
-def _matrix(t, rows, cols, name, dtypes, dev):
+def _matrix(t, rows, cols, name, dtype, dev):
     """Pointer and row stride of a [>= rows][>= cols] tensor whose rows are contiguous."""
-    _cuda(t, name, dtypes, dev)
+    if not isinstance(t, _torch().Tensor) or t.get_device() != dev or t.dtype != dtype:
+        _refuse(t, name, dtype, dev)
     shape = t.shape
     if len(shape) != 2 or shape[0] < rows or shape[1] < cols:
         raise ValueError(f"{name} must be at least [{rows}][{cols}], got {list(shape)}")
@@ -660,11 +666,12 @@ def _matrix(t, rows, cols, name, dtypes, dev):
     return t.data_ptr(), ld
 
 
-def _vector(t, n, name, dtypes, dev):
+def _vector(t, n, name, dtype, dev):
     """Pointer of a contiguous tensor of at least n values; None stays None."""
     if t is None:
         return None
-    _cuda(t, name, dtypes, dev)
+    if not isinstance(t, _torch().Tensor) or t.get_device() != dev or t.dtype != dtype:
+        _refuse(t, name, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.numel() < n:
@@ -673,15 +680,7 @@ def _vector(t, n, name, dtypes, dev):
 
 
 def _device() -> int:
-    return _torch().cuda.current_device()
-
-
-def _types(code: int):
-    return (_act_dtype(code),)
-
-
-def _f32():
-    return (_torch().float32,)
+    return _torch()._C._cuda_getDevice()
 
 
 class Linear:
@@ -703,7 +702,7 @@ def make_linear_config(n, k, alpha=0.6, in_dtype=MOE_BF16, out_dtype=MOE_BF16) -
 
 
 def moe_w8a8_linear_prepare(cfg: moe_w8a8_linear_config, w, bias=None, act_absmax=None, stream=None) -> Linear:
-    dev, f32 = _device(), _f32()
+    dev, f32 = _device(), _torch().float32
     h = ctypes.c_void_p()
     _check(lib().moe_w8a8_linear_prepare(
         ctypes.byref(cfg), _vector(w, cfg.k * cfg.n, "w", f32, dev), _vector(bias, cfg.n, "bias", f32, dev),
@@ -713,10 +712,10 @@ def moe_w8a8_linear_prepare(cfg: moe_w8a8_linear_config, w, bias=None, act_absma
 
 
 def moe_w8a8_linear_prepare_codes(cfg: moe_w8a8_linear_config, wq, sw, bias=None, inv_s=None, stream=None) -> Linear:
-    dev, f32 = _device(), _f32()
+    dev, f32 = _device(), _torch().float32
     h = ctypes.c_void_p()
     _check(lib().moe_w8a8_linear_prepare_codes(
-        ctypes.byref(cfg), _vector(wq, cfg.n * cfg.k, "wq", (_torch().int8,), dev), _vector(sw, cfg.n, "sw", f32, dev),
+        ctypes.byref(cfg), _vector(wq, cfg.n * cfg.k, "wq", _torch().int8, dev), _vector(sw, cfg.n, "sw", f32, dev),
         _vector(bias, cfg.n, "bias", f32, dev), _vector(inv_s, cfg.k, "inv_s", f32, dev), _stream(stream),
         ctypes.byref(h)), "moe_w8a8_linear_prepare_codes")
     return Linear(h, cfg, inv_s is not None)
@@ -730,10 +729,10 @@ def moe_w8a8_linear_forward(l: Linear, x, T: int, y, workspace, stream=None):
     c, dev = l.cfg, _device()
     if T == 0:
         return
-    xp, ldx = _matrix(x, T, c.k, "x", _types(c.in_dtype), dev)
-    yp, ldy = _matrix(y, T, c.n, "y", _types(c.out_dtype), dev)
+    xp, ldx = _matrix(x, T, c.k, "x", _act_dtype(c.in_dtype), dev)
+    yp, ldy = _matrix(y, T, c.n, "y", _act_dtype(c.out_dtype), dev)
     _check(lib().moe_w8a8_linear_forward(l.handle, xp, ldx, T, yp, ldy, _vector(workspace, 0, "workspace",
-                                                                                (workspace.dtype,), dev),
+                                                                                workspace.dtype, dev),
                                          _nbytes(workspace), _stream(stream)), "moe_w8a8_linear_forward")
 
 
@@ -741,9 +740,9 @@ def moe_w8a8_linear_forward_codes(l: Linear, xq, sx, T: int, y, stream=None):
     c, dev = l.cfg, _device()
     if T == 0:
         return
-    qp, ldq = _matrix(xq, T, c.k, "xq", (_torch().int8,), dev)
-    yp, ldy = _matrix(y, T, c.n, "y", _types(c.out_dtype), dev)
-    _check(lib().moe_w8a8_linear_forward_codes(l.handle, qp, ldq, _vector(sx, T, "sx", _f32(), dev), T, yp, ldy,
+    qp, ldq = _matrix(xq, T, c.k, "xq", _torch().int8, dev)
+    yp, ldy = _matrix(y, T, c.n, "y", _act_dtype(c.out_dtype), dev)
+    _check(lib().moe_w8a8_linear_forward_codes(l.handle, qp, ldq, _vector(sx, T, "sx", _torch().float32, dev), T, yp, ldy,
                                                _stream(stream)), "moe_w8a8_linear_forward_codes")
 
 
@@ -774,39 +773,40 @@ def moe_w8a8_block_norm(cfg: moe_w8a8_norm_config, T: int, b=None, x=None, gate=
                         inv_s=None, x_out=None, n_out=None, xq=None, sx=None, stream=None):
     if T == 0:
         return
-    dev, d, f32 = _device(), cfg.d, _f32()
-    res = _types(cfg.res_dtype)
+    dev, d, f32 = _device(), cfg.d, _torch().float32
+    res = _act_dtype(cfg.res_dtype)
     none = (None, 0)
     gp, ldg = none
     if gate is not None:
         if cfg.gate == MOE_GATE_ELEMENT:
-            gp, ldg = _matrix(gate, T, d, "gate", _types(cfg.in_dtype), dev)
+            gp, ldg = _matrix(gate, T, d, "gate", _act_dtype(cfg.in_dtype), dev)
         else:
             gp = _vector(gate, T if cfg.gate == MOE_GATE_TOKEN else d, "gate", f32, dev)
     io = moe_w8a8_norm_io(
-        *(none if b is None else _matrix(b, T, d, "b", _types(cfg.in_dtype), dev)),
+        *(none if b is None else _matrix(b, T, d, "b", _act_dtype(cfg.in_dtype), dev)),
         *(none if x is None else _matrix(x, T, d, "x", res, dev)), gp, ldg, _vector(w_post, d, "w_post", f32, dev),
         _vector(w_pre, d, "w_pre", f32, dev), _vector(inv_s, d, "inv_s", f32, dev),
         *(none if x_out is None else _matrix(x_out, T, d, "x_out", res, dev)),
-        *(none if n_out is None else _matrix(n_out, T, d, "n_out", _types(cfg.out_dtype), dev)),
-        *(none if xq is None else _matrix(xq, T, d, "xq", (_torch().int8,), dev)), _vector(sx, T, "sx", f32, dev))
+        *(none if n_out is None else _matrix(n_out, T, d, "n_out", _act_dtype(cfg.out_dtype), dev)),
+        *(none if xq is None else _matrix(xq, T, d, "xq", _torch().int8, dev)), _vector(sx, T, "sx", f32, dev))
     _check(lib().moe_w8a8_block_norm(ctypes.byref(cfg), ctypes.byref(io), T, _stream(stream)), "moe_w8a8_block_norm")
 
 
 def moe_w8a8_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, allowed=None, prob=None,
                     stream=None):
     torch = _torch()
-    dev, f32, i32 = _device(), _f32(), (torch.int32,)
+    dev, f32, i32 = _device(), torch.float32, torch.int32
     rows, vocab = logits.shape
     if rows == 0:
         return
-    lp, ld = _matrix(logits, rows, vocab, "logits", (torch.float32, torch.bfloat16), dev)
+    bf16 = logits.dtype == torch.bfloat16
+    lp, ld = _matrix(logits, rows, vocab, "logits", torch.bfloat16 if bf16 else f32, dev)
     ap, lda = (None, 0) if allowed is None else _matrix(allowed, rows, (vocab + 31) // 32, "allowed", i32, dev)
     io = moe_w8a8_sample_io(
         lp, ld, ap, lda, _vector(temperature, rows, "temperature", f32, dev), _vector(top_k, rows, "top_k", i32, dev),
         _vector(top_p, rows, "top_p", f32, dev), _vector(min_p, rows, "min_p", f32, dev), _vector(u, rows, "u", f32, dev),
         _vector(token, rows, "token", i32, dev), _vector(prob, rows, "prob", f32, dev))
-    _check(lib().moe_w8a8_sample(ctypes.byref(io), rows, vocab, MOE_BF16 if logits.dtype == torch.bfloat16 else MOE_F32,
+    _check(lib().moe_w8a8_sample(ctypes.byref(io), rows, vocab, MOE_BF16 if bf16 else MOE_F32,
                                  _stream(stream)), "moe_w8a8_sample")
 
 
