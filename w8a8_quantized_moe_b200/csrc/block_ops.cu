@@ -205,6 +205,11 @@ moe_status moe_w8a8_linear_forward(const moe_w8a8_linear* l, const void* x, int6
         misaligned(workspace, kAlign) || !on_device(l))
         return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < moe_w8a8_linear_workspace_size(l, T)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (linear_quantizes(l->tiles, x, ldx, T, c.in_dtype))
+        return launch_linear_quantizing(l->tiles, x, ldx, c.in_dtype, l->inv_s, T, y, ldy, c.out_dtype,
+                                        (cudaStream_t)stream) == cudaSuccess
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
     NormParams q{};
     q.T = T;
     q.d = c.k;

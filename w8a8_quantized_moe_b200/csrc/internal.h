@@ -272,6 +272,13 @@ cudaError_t launch_linear_untile(const LinearTiles& t, int8_t* wq, cudaStream_t 
 cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, const float* sx, int T, void* y, int64_t ldy,
                           int out_dtype, cudaStream_t s);
 
+// A few tokens straight from activations, quantised inside the product's kernel;
+// whether a call can take that way (else launch_block_norm and launch_linear).
+constexpr int kLinearQuantTokens = 4;
+bool linear_quantizes(const LinearTiles& t, const void* x, int64_t ldx, int T, int in_dtype);
+cudaError_t launch_linear_quantizing(const LinearTiles& t, const void* x, int64_t ldx, int in_dtype, const float* inv_s,
+                                     int T, void* y, int64_t ldy, int out_dtype, cudaStream_t s);
+
 struct NormParams {
     int64_t T;
     int d, in_dtype, res_dtype, out_dtype, gate_kind, gate_sigmoid;

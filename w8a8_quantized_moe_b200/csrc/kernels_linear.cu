@@ -128,7 +128,12 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t tmem_d, uint64_t adesc, uin
 }
 
 struct LinearParams {
-    int n, T, kb;             // channels, tokens, input tiles
+    int n, k, T, kb;          // channels, inputs, tokens, input tiles
+    int stages;               // small kernel: ring stages
+    const void* x;            // small kernel, quantising: the activations
+    const float* inv_s;
+    int64_t ldx;
+    int in_dtype;
     int n_tiles, m_tiles;     // pair kernel: 256-channel and 256-token tiles
     const float *sw, *bias, *sx;
     void* y;
@@ -142,48 +147,130 @@ struct LinearParams {
 // TN tokens per block, the weights' 128 channels as the MMA's M.  Block (x, y)
 // of the grid: channel tile x / S of cluster rank x % S, tokens [y TN, + TN).
 // The S blocks of a cluster take contiguous parts of the input tiles.
-//   warp 0   TMA producer: one weight tile and the tokens' 128 codes per stage.
-//            The weights are constants of the handle, so their first copies are
-//            issued before the previous kernel's results are waited for.
+//   warp 0   TMA producer: weight tiles (and, from codes, the tokens' 128 codes)
+//            into a ring.  The weights are constants of the handle, so their
+//            first copies are issued before the previous kernel's results are
+//            waited for.
 //   warp 1   tensor memory and the MMAs
-//   all 4    accumulators (lane = channel) to shared memory as [token][channel]
+//   all 8    accumulators (lane = channel) to shared memory as [token][channel]
 //            words; then each block of the cluster adds the S partial tiles of
 //            its part of the tokens and writes whole rows.
-template <int TN>
-struct SmallCfg {
-    static constexpr int kStageBytes = kTileBytes + TN * kTile;
-    static constexpr int kStages = TN <= 32 ? 5 : TN == 64 ? 4 : 3;   // two blocks per SM
-    static constexpr uint32_t kCols = TN < 32 ? 32 : TN;
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
-    static_assert(TN * kTile * 4 <= kStages * kStageBytes, "the partial tile reuses the stages");
-};
+// QUANT: from the activations of at most kLinearQuantTokens tokens.  Each block
+// finds the tokens' scales itself and quantises its own part of the inputs while
+// its weights are on their way: one launch instead of two, at the price of every
+// block reading the tokens.
+constexpr int kSmallThreads = 256;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallMaxStages = 4;
+constexpr int kSmallMaxSplit = 8;
+constexpr size_t kSmallMaxSmem = 220 * 1024;   // beside the static part
 
-template <int NS>
 struct SmallCtl {
-    uint64_t full[NS], empty[NS], acc;
+    uint64_t full[kSmallMaxStages], empty[kSmallMaxStages], acc;
     uint32_t tmem_base;
     int abort;
+    uint32_t amax[kSmallWarps][kLinearQuantTokens];   // QUANT: the warps' largest values (bits), then ...
+    float scale[kLinearQuantTokens];                  // ... the tokens' scales
 };
 
-constexpr int kSmallThreads = 128;
+template <int TN, bool QUANT>
+__host__ __device__ constexpr int small_stage_bytes() { return kTileBytes + (QUANT ? 0 : TN * kTile); }
+// Shared memory of a block with `stages` ring stages and (QUANT) nkb input tiles
+// of codes; the partial tile reuses it from its start.
+template <int TN, bool QUANT>
+constexpr size_t small_smem(int stages, int nkb) {
+    const size_t operands = (size_t)stages * small_stage_bytes<TN, QUANT>() + (QUANT ? (size_t)nkb * TN * kTile : 0);
+    const size_t part = (size_t)TN * kTile * 4;
+    return (operands > part ? operands : part) + 1024;
+}
+
+// QUANT: the codes of this block's part of the inputs, [input tile][token][128
+// codes] in the 128-byte swizzle (16-byte chunks XOR the row), and the tokens'
+// scales.  The part's values are loaded first and stay in registers.
+constexpr int kOwnGroups = 4;   // groups of 8 values of the part per thread
+
+__device__ __forceinline__ void small_load(const LinearParams& p, int t, int j, float (&v)[8]) {
+    load8_act(p.x, (int64_t)t * p.ldx + j, p.in_dtype, v);
+    if (p.inv_s) {
+        const float4 a = *reinterpret_cast<const float4*>(p.inv_s + j), b = *reinterpret_cast<const float4*>(p.inv_s + j + 4);
+        const float s[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = __fmul_rn(v[c], s[c]);
+    }
+}
 
 template <int TN>
+__device__ __forceinline__ void small_quantize(const LinearParams& p, SmallCtl* ctl, uint8_t* codes, int kb0, int nkb) {
+    const int groups = nkb * (kTile / 8);
+    float own[kOwnGroups][8];
+#pragma unroll
+    for (int i = 0; i < kOwnGroups; ++i) {
+        const int at = threadIdx.x + i * kSmallThreads, t = at / groups, j = kb0 * kTile + at % groups * 8;
+        if (t < p.T && j < p.k) {
+            small_load(p, t, j, own[i]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) own[i][c] = 0.0f;   // inputs past the last one
+        }
+    }
+    for (int t = 0; t < p.T; ++t) {
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int j = threadIdx.x * 8; j < p.k; j += kSmallThreads * 8) {
+            float v[8];
+            small_load(p, t, j, v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) m = max(m, __float_as_uint(fabsf(v[c])));
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if ((threadIdx.x & 31) == 0) ctl->amax[threadIdx.x >> 5][t] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < p.T) {
+        uint32_t m = 0;
+        for (int w = 0; w < kSmallWarps; ++w) m = max(m, ctl->amax[w][threadIdx.x]);
+        // a token that holds an infinity or a NaN gets codes 0 and the scale NaN
+        ctl->scale[threadIdx.x] = m < 0x7f800000u ? __fdiv_rn(__uint_as_float(m), 127.0f) : __int_as_float(0x7fc00000);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kOwnGroups; ++i) {
+        const int at = threadIdx.x + i * kSmallThreads, t = at / groups, g = at % groups;
+        if (t >= p.T) break;
+        const float s = ctl->scale[t];
+        uint2 q = make_uint2(0u, 0u);
+        if (s > 0.0f) {
+            const float inv = __frcp_rn(s);
+            q = make_uint2(fmt_codes4<FMT_INT8>(own[i][0], own[i][1], own[i][2], own[i][3], s, inv),
+                           fmt_codes4<FMT_INT8>(own[i][4], own[i][5], own[i][6], own[i][7], s, inv));
+        }
+        const int chunk = (g >> 1) & 7;
+        *reinterpret_cast<uint2*>(codes + (size_t)(g >> 4) * TN * kTile + t * kTile + ((chunk ^ (t & 7)) << 4) + (g & 1) * 8) = q;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+}
+
+template <int TN, bool QUANT>
 __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                                      const __grid_constant__ CUtensorMap tm_x,
                                                                      const LinearParams p) {
-    using C = SmallCfg<TN>;
+    constexpr int kStageBytes = small_stage_bytes<TN, QUANT>();
+    constexpr uint32_t kCols = TN < 32 ? 32 : TN;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
+    __shared__ SmallCtl shared_ctl;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    SmallCtl<C::kStages>* ctl = reinterpret_cast<SmallCtl<C::kStages>*>(smem + C::kStages * C::kStageBytes);
+    SmallCtl* ctl = &shared_ctl;
     cg::cluster_group cl = cg::this_cluster();
     const int S = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nt = blockIdx.x / S, t0 = blockIdx.y * TN;
+    const int nt = blockIdx.x / S, t0 = blockIdx.y * TN, tn = min(TN, p.T - t0);
     const int kb0 = (int)((int64_t)p.kb * rank / S), kb1 = (int)((int64_t)p.kb * (rank + 1) / S);
-    const int nkb = kb1 - kb0;
+    const int nkb = kb1 - kb0, stages = p.stages;
+    uint8_t* codes = smem + stages * kStageBytes;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
         }
@@ -193,7 +280,7 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl->tmem_base)),
-                     "r"(C::kCols));
+                     "r"(kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     pdl_trigger();
@@ -203,42 +290,50 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort = &ctl->abort;
 
+    auto load_w = [&](int i) {
+        const int s = i % stages;
+        mbar_arrive_expect_tx(&ctl->full[s], kStageBytes);
+        tma_load_2d(smem + s * kStageBytes, &tm_w, &ctl->full[s], 0, (nt * p.kb + kb0 + i) * kTile);
+    };
+    const int first = min(nkb, stages);
+    if (threadIdx.x == 0)
+        for (int i = 0; i < first; ++i) load_w(i);
+    __syncwarp();
+    if (QUANT) {
+        pdl_wait();
+        small_quantize<TN>(p, ctl, codes, kb0, nkb);
+    }
     if (warp == 0) {
         if (lane == 0) {
-            const int first = min(nkb, C::kStages);
-            auto load_w = [&](int i) {
-                const int s = i % C::kStages;
-                mbar_arrive_expect_tx(&ctl->full[s], C::kStageBytes);
-                tma_load_2d(smem + s * C::kStageBytes, &tm_w, &ctl->full[s], 0, (nt * p.kb + kb0 + i) * kTile);
-            };
             auto load_x = [&](int i) {
-                const int s = i % C::kStages;
-                tma_load_2d(smem + s * C::kStageBytes + kTileBytes, &tm_x, &ctl->full[s], (kb0 + i) * kTile, t0);
+                const int s = i % stages;
+                tma_load_2d(smem + s * kStageBytes + kTileBytes, &tm_x, &ctl->full[s], (kb0 + i) * kTile, t0);
             };
-            for (int i = 0; i < first; ++i) load_w(i);
-            pdl_wait();
-            for (int i = 0; i < first; ++i) load_x(i);
+            if (!QUANT) {
+                pdl_wait();
+                for (int i = 0; i < first; ++i) load_x(i);
+            }
             int issued = first;
             for (int i = first; i < nkb; ++i) {
-                if (!mbar_wait(&ctl->empty[i % C::kStages], ((i / C::kStages) - 1) & 1, abort, p.status, 1, i)) break;
+                if (!mbar_wait(&ctl->empty[i % stages], ((i / stages) - 1) & 1, abort, p.status, 1, i)) break;
                 load_w(i);
-                load_x(i);
+                if (!QUANT) load_x(i);
                 ++issued;
             }
             // every copy has landed before the stages are reused or the block ends (bounded)
-            for (int i = max(0, issued - C::kStages); i < issued; ++i) {
+            for (int i = max(0, issued - stages); i < issued; ++i) {
                 const uint64_t b = global_timer();
-                while (!mbar_try_wait(&ctl->full[i % C::kStages], (i / C::kStages) & 1) &&
-                       global_timer() - b < kWaitBudgetNs) {}
+                while (!mbar_try_wait(&ctl->full[i % stages], (i / stages) & 1) && global_timer() - b < kWaitBudgetNs) {}
             }
         }
     } else if (warp == 1) {
         if (lane == 0) {
             for (int i = 0; i < nkb; ++i) {
-                const int s = i % C::kStages;
-                if (!mbar_wait(&ctl->full[s], (i / C::kStages) & 1, abort, p.status, 3, i)) break;
+                const int s = i % stages;
+                if (!mbar_wait(&ctl->full[s], (i / stages) & 1, abort, p.status, 3, i)) break;
                 tc_fence_after();
-                const uint32_t a = smem_u32(smem + s * C::kStageBytes), b = a + kTileBytes;
+                const uint32_t a = smem_u32(smem + s * kStageBytes);
+                const uint32_t b = QUANT ? smem_u32(codes + (size_t)i * TN * kTile) : a + kTileBytes;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 32; ++kk)
                     mma_i8<idesc_i8(kTile, TN)>(tmem, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), (i | kk) != 0);
@@ -253,43 +348,45 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
     __syncthreads();   // the stages are free: every copy and MMA is done
     tc_fence_after();
 
-    // partial tile [token][channel], 128 words per row
+    // partial tile [token][channel], 128 words per row; two warps share a lane quarter
     int32_t* part = reinterpret_cast<int32_t*>(smem);
-    const int ch = warp * 32 + lane;
-    const int tn = min(TN, p.T - t0);   // tokens of this block
-    constexpr int kChunk = TN < 32 ? TN : 32;
+    const int quad = warp & 3, half = warp >> 2, ch = quad * 32 + lane;
+    constexpr int kHalf = TN < 32 ? TN : TN / 2, kChunk = kHalf < 32 ? kHalf : 32;
+    if (TN >= 32 || half == 0) {
 #pragma unroll
-    for (int c = 0; c < TN / kChunk; ++c) {
-        uint32_t v[kChunk];
-        const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + c * kChunk;
-        if constexpr (kChunk == 16)
-            tmem_ld16(at, v);
-        else
-            tmem_ld32(at, v);
-        tmem_ld_wait();
+        for (int c = 0; c < kHalf / kChunk; ++c) {
+            uint32_t v[kChunk];
+            const int col = half * kHalf + c * kChunk;
+            const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + col;
+            if constexpr (kChunk == 16)
+                tmem_ld16(at, v);
+            else
+                tmem_ld32(at, v);
+            tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) part[(c * kChunk + j) * kTile + ch] = ok && nkb > 0 ? (int)v[j] : 0;
+            for (int j = 0; j < kChunk; ++j) part[(col + j) * kTile + ch] = ok && nkb > 0 ? (int)v[j] : 0;
+        }
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
     }
-    cl.sync();
+    if (S > 1) cl.sync();
     // this block's part of the tokens; four channels per thread
     const int r0 = tn * rank / S, r1 = tn * (rank + 1) / S;
-    const int c4 = (threadIdx.x & 31) * 4, n0 = nt * kTile + c4;
+    const int c4 = lane * 4, n0 = nt * kTile + c4;
     const float4 sw = *reinterpret_cast<const float4*>(p.sw + n0);
     const float4 bs = p.bias ? *reinterpret_cast<const float4*>(p.bias + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = r0 + warp; r < r1; r += kSmallThreads / 32) {
+    for (int r = r0 + warp; r < r1; r += kSmallWarps) {
         int4 a = make_int4(0, 0, 0, 0);
         for (int b = 0; b < S; ++b) {
             const int4 q = *reinterpret_cast<const int4*>(cl.map_shared_rank(part, b) + r * kTile + c4);
             a.x += q.x, a.y += q.y, a.z += q.z, a.w += q.w;
         }
         const int64_t t = t0 + r;
-        const float sx = p.sx[t];
+        const float sx = QUANT ? ctl->scale[r] : p.sx[t];
         const float y0 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.x), sx), sw.x), bs.x);
         const float y1 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.y), sx), sw.y), bs.y);
         const float y2 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.z), sx), sw.z), bs.z);
@@ -318,7 +415,7 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
             }
         }
     }
-    cl.sync();   // no block leaves while another reads its partial tile
+    if (S > 1) cl.sync();   // no block leaves while another reads its partial tile
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -517,13 +614,28 @@ bool make_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN>
-cudaError_t launch_small(const LinearTiles& t, const CUtensorMap& tx, const LinearParams& p, int split, cudaStream_t s) {
+template <int TN, bool QUANT>
+cudaError_t launch_small_as(const LinearTiles& t, const CUtensorMap& tx, LinearParams& p, int split, cudaStream_t s) {
+    // the ring: what the block reads, four stages at most (fewer where two blocks would
+    // not fit on an SM: 64 x 4096 x 32000 took 25.3 us with four, 34.6 with six)
+    const int nkb = (t.kb + split - 1) / split;
+    p.stages = std::min(nkb, kSmallMaxStages);
+    while (p.stages > 2 && small_smem<TN, QUANT>(p.stages, nkb) > kSmallMaxSmem / 2) --p.stages;
+    const size_t smem = small_smem<TN, QUANT>(p.stages, nkb);
     static std::atomic<uint64_t> attr{0};
-    cudaError_t e = smem_attr_once(linear_small_kernel<TN>, SmallCfg<TN>::kSmem, attr);
+    cudaError_t e = smem_attr_once(linear_small_kernel<TN, QUANT>, kSmallMaxSmem, attr);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)((t.n + kTile - 1) / kTile * split), (unsigned)((p.T + TN - 1) / TN));
-    return launch_cluster(linear_small_kernel<TN>, grid, dim3(kSmallThreads), split, SmallCfg<TN>::kSmem, s, t.tm_w, tx, p);
+    return launch_cluster(linear_small_kernel<TN, QUANT>, grid, dim3(kSmallThreads), split, smem, s, t.tm_w, tx, p);
+}
+
+cudaError_t launch_small(const LinearTiles& t, const CUtensorMap& tx, LinearParams& p, int tn, int split, cudaStream_t s) {
+    switch (tn) {
+        case 16: return launch_small_as<16, false>(t, tx, p, split, s);
+        case 32: return launch_small_as<32, false>(t, tx, p, split, s);
+        case 64: return launch_small_as<64, false>(t, tx, p, split, s);
+        default: return launch_small_as<128, false>(t, tx, p, split, s);
+    }
 }
 
 cudaError_t pair_clusters(int* out) {
@@ -582,15 +694,32 @@ cudaError_t launch_linear_untile(const LinearTiles& t, int8_t* wq, cudaStream_t 
     return cudaGetLastError();
 }
 
-cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, const float* sx, int T, void* y, int64_t ldy,
-                          int out_dtype, cudaStream_t s) {
+namespace {
+
+int small_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+// Split the inputs while the blocks are at most two per SM (three on two SMs from
+// 64 tokens up), four input tiles each at least.  (A block takes in 50 GB/s at
+// most, so all SMs have to read; past two blocks per SM the rest waits for a second
+// round.  Device time of one call from codes, us, split by 1, 2, 4, 8: 1 x 4096 x
+// 4096 13.1, 8.5, 5.9, 5.6; 32 x 4096 x 6144 14.3, 9.4, 7.2, 12.1; 64 x 4096 x 4096
+// 16.0, 10.7, 7.9, 8.6; 64 x 4096 x 32000 25.3, 32.4, 40.3, 64.1.)
+int small_split(const LinearTiles& t, int T, int tn) {
+    const int64_t blocks = (int64_t)((t.n + kTile - 1) / kTile) * ((T + tn - 1) / tn);
+    const int64_t most = tn <= 32 ? 2 * t.num_sms : t.num_sms + t.num_sms / 2;
+    int split = 1;
+    while (split < kSmallMaxSplit && blocks * split * 2 <= most && t.kb / (split * 2) >= 4) split *= 2;
+    return split;
+}
+
+LinearParams linear_params(const LinearTiles& t, int T, void* y, int64_t ldy, int out_dtype) {
     LinearParams p{};
     p.n = t.n;
+    p.k = t.k;
     p.T = T;
     p.kb = t.kb;
     p.sw = t.sw;
     p.bias = t.bias;
-    p.sx = sx;
     p.y = y;
     p.ldy = ldy;
     p.out_bf16 = out_dtype == MOE_BF16;
@@ -598,7 +727,33 @@ cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, c
     p.status = t.status;
     p.n_tiles = (t.n + 255) / 256;
     p.m_tiles = (T + 255) / 256;
-    const int tn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    return p;
+}
+
+}  // namespace
+
+bool linear_quantizes(const LinearTiles& t, const void* x, int64_t ldx, int T, int in_dtype) {
+    const int64_t esz = in_dtype == MOE_BF16 ? 2 : 4;
+    if (t.k % 8 || ((uintptr_t)x & 15) || (ldx * esz) % 16 || T > kLinearQuantTokens) return false;
+    const int split = small_split(t, T, 16), nkb = (t.kb + split - 1) / split;
+    return T * nkb * (kTile / 8) <= kOwnGroups * kSmallThreads;   // the part's values fit the threads' registers
+}
+
+cudaError_t launch_linear_quantizing(const LinearTiles& t, const void* x, int64_t ldx, int in_dtype, const float* inv_s,
+                                     int T, void* y, int64_t ldy, int out_dtype, cudaStream_t s) {
+    LinearParams p = linear_params(t, T, y, ldy, out_dtype);
+    p.x = x;
+    p.ldx = ldx;
+    p.in_dtype = in_dtype;
+    p.inv_s = inv_s;
+    return launch_small_as<16, true>(t, t.tm_w, p, small_split(t, T, 16), s);   // (no map of x)
+}
+
+cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, const float* sx, int T, void* y, int64_t ldy,
+                          int out_dtype, cudaStream_t s) {
+    LinearParams p = linear_params(t, T, y, ldy, out_dtype);
+    p.sx = sx;
+    const int tn = small_tokens(T);
     const int64_t pair_tiles = (int64_t)p.n_tiles * p.m_tiles;
     const bool pairs = T > 128 && pair_tiles * 2 >= t.num_sms;
     CUtensorMap tx;
@@ -613,16 +768,7 @@ cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, c
         const int grid = 2 * (int)std::min<int64_t>(nc, pair_tiles);
         return launch_pdl(linear_pair_kernel, dim3(grid), dim3(kPThreads), kPSmem, s, t.tm_w, tx, p);
     }
-    // split the inputs until every SM has two blocks, four input tiles each at least
-    const int64_t blocks = (int64_t)((t.n + kTile - 1) / kTile) * ((T + tn - 1) / tn);
-    int split = 1;
-    while (split < 8 && blocks * split * 2 <= 2 * t.num_sms && t.kb / (split * 2) >= 4) split *= 2;
-    switch (tn) {
-        case 16: return launch_small<16>(t, tx, p, split, s);
-        case 32: return launch_small<32>(t, tx, p, split, s);
-        case 64: return launch_small<64>(t, tx, p, split, s);
-        default: return launch_small<128>(t, tx, p, split, s);
-    }
+    return launch_small(t, tx, p, tn, small_split(t, T, tn), s);
 }
 
 }  // namespace moe
