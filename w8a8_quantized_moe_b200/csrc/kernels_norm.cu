@@ -13,9 +13,9 @@
 //
 // Bound by memory: every value is read once and written once, and a row stays
 // in registers between its two norms.  Two kernels: block_norm_rows_kernel for
-// rows on 16-byte boundaries whose stream and branch have one type (16-byte
-// accesses; the blocks stay and load their next row before they work on the
-// current one), block_norm_kernel for everything else.
+// many rows on 16-byte boundaries, bound by memory and instructions, with few
+// threads per row; block_norm_kernel for a few rows, bound by latency, with many,
+// and for every type, stride and size.
 #include "common.cuh"
 #include "internal.h"
 
@@ -66,6 +66,12 @@ __device__ __forceinline__ void store_vals(void* p, int64_t i, int dtype, const 
     }
 }
 
+__device__ __forceinline__ float warp_sum_f(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // Sum and unsigned maximum over the TPR threads of a row.  `red`: 2 words per
 // warp of the block, used by one call at a time (the caller alternates halves).
 template <int TPR>
@@ -95,27 +101,73 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& mx, float* red)
     }
 }
 
-// The codes of four values for scale s > 0 (inv = fp32(1 / s)): identical to
+// Pairs of fp32 values: one instruction for two of each operation, each rounded
+// as alone.
+struct Pair {
+    uint64_t v;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// The larger magnitude, a NaN if there is one.
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+// The codes of eight values for scale s > 0 (inv = fp32(1 / s)): identical to
 // quant_code of each.  t = v inv is within 2.3e-5 of the IEEE quotient where that
 // is below 128 (quant_code_fast), so unless t lies within 3e-5 of a half-integer
 // both round to the same integer, which the sum with 1.5 x 2^23 leaves in its low
 // byte; the largest value has the quotient 127 and a rounding, so no clamp is
 // needed.  Otherwise (or when 1 / s overflowed: the comparison fails) the
 // quotients are formed.
-__device__ __forceinline__ uint32_t int8_codes4(float v0, float v1, float v2, float v3, float s, float inv) {
-    const float v[4] = {v0, v1, v2, v3};
-    float a[4];
-    bool fast = true;
+__device__ __forceinline__ uint2 int8_codes8(const Pair (&v)[4], float s, float inv) {
+    const Pair magic(12582912.0f, 12582912.0f), minus(-12582912.0f, -12582912.0f), one(-1.0f, -1.0f), r(inv, inv);
+    float a[8];
+    float off = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float t = __fmul_rn(v[i], inv);
-        a[i] = __fadd_rn(t, 12582912.0f);
-        fast = fast && fabsf(__fsub_rn(t, __fsub_rn(a[i], 12582912.0f))) < 0.49997f;
+        const Pair t = v[i] * r;
+        const Pair sum = t + magic;
+        float d0, d1;
+        fma2(sum + minus, one, t).get(d0, d1);   // t less the integer next to it
+        off = max_abs_nan(max_abs_nan(off, d0), d1);
+        sum.get(a[2 * i], a[2 * i + 1]);
     }
-    if (fast)
-        return __byte_perm(__byte_perm(__float_as_uint(a[0]), __float_as_uint(a[1]), 0x0040),
-                           __byte_perm(__float_as_uint(a[2]), __float_as_uint(a[3]), 0x0040), 0x5410);
-    return pack4(quant_code(v0, s), quant_code(v1, s), quant_code(v2, s), quant_code(v3, s));
+    uint32_t q[2];
+    if (off < 0.49997f) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            q[i] = __byte_perm(__byte_perm(__float_as_uint(a[4 * i]), __float_as_uint(a[4 * i + 1]), 0x0040),
+                               __byte_perm(__float_as_uint(a[4 * i + 2]), __float_as_uint(a[4 * i + 3]), 0x0040), 0x5410);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float e[4];
+            v[2 * i].get(e[0], e[1]);
+            v[2 * i + 1].get(e[2], e[3]);
+            q[i] = pack4(quant_code(e[0], s), quant_code(e[1], s), quant_code(e[2], s), quant_code(e[3], s));
+        }
+    }
+    return make_uint2(q[0], q[1]);
 }
 
 // TPR threads per row, each with G groups of W values: group g of thread t is
@@ -243,10 +295,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
             if (p.xq) {
                 int8_t* dst = p.xq + row * p.ldq + at;
                 if constexpr (W == 8) {
-                    *reinterpret_cast<uint2*>(dst) =
-                        s > 0.0f ? make_uint2(int8_codes4(b[g][0], b[g][1], b[g][2], b[g][3], s, inv),
-                                              int8_codes4(b[g][4], b[g][5], b[g][6], b[g][7], s, inv))
-                                 : make_uint2(0u, 0u);
+                    const Pair v[4] = {Pair(b[g][0], b[g][1]), Pair(b[g][2], b[g][3]), Pair(b[g][4], b[g][5]), Pair(b[g][6], b[g][7])};
+                    *reinterpret_cast<uint2*>(dst) = s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
                 } else {
                     *dst = s > 0.0f ? (int8_t)quant_code_fast(b[g][0], s, inv) : (int8_t)0;
                 }
@@ -268,13 +318,24 @@ struct Raw8<true> {
     __device__ __forceinline__ void load(const void* p, int64_t i) {
         q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i);
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = q;
+    }
+    __device__ __forceinline__ void get(Pair (&v)[4]) const {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = Pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+    __device__ __forceinline__ void set(const Pair (&v)[4]) {   // rounds
+        uint32_t w[4];
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            float a, b;
+            v[i].get(a, b);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        q = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 template <>
@@ -285,158 +346,174 @@ struct Raw8<false> {
         a = q[0];
         b = q[1];
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+        q[0] = a;
+        q[1] = b;
+    }
+    __device__ __forceinline__ void get(Pair (&v)[4]) const {
+        v[0] = Pair(a.x, a.y);
+        v[1] = Pair(a.z, a.w);
+        v[2] = Pair(b.x, b.y);
+        v[3] = Pair(b.z, b.w);
+    }
+    __device__ __forceinline__ void set(const Pair (&v)[4]) {
+        v[0].get(a.x, a.y);
+        v[1].get(a.z, a.w);
+        v[2].get(b.x, b.y);
+        v[3].get(b.z, b.w);
     }
 };
+
+// 8 fp32 weights (plus `offset`).
+__device__ __forceinline__ void load_weights(const float* p, int at, float offset, Pair (&w)[4]) {
+    Raw8<false> q;
+    q.load(p, at);
+    q.get(w);
+    if (offset != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = w[i] + Pair(offset, offset);
+    }
+}
 
 __device__ __forceinline__ float gate_value(const NormParams& p, float g) {
     return p.gate_sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
-// Rows on 16-byte boundaries.  A block (a warp for TPR = 32) takes every
-// gridDim-th row; the loads of its next row are in flight while it works on the
-// current one.  Thread t owns values [(t + TPR g) 8, + 8), g < G.
-// BRANCH, POST, GATED, CODES: b, w_post, a gate and xq are given.  Measured against one block
-// per row without the early loads, and 16 instead of 9 instructions per code:
-// 16384 x 8192 bf16 with residual add and norm 299 -> %NL% us, the quantisation of
-// 16384 x 4096 in front of a product %QB% -> %QA% us.
-template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool GATED, bool CODES>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, TPR == 32 ? 4 : 1024 / TPR)
-    block_norm_rows_kernel(const NormParams p) {
+// Many rows on 16-byte boundaries, stream and branch of one type.  TPR threads
+// per row (a warp, or a block of that many), G groups of 8 values each: thread t
+// owns values [(t + TPR g) 8, + 8).  Few threads with many values each, so that a
+// row's fixed work (two reductions, a division) is shared by many values; the row
+// is kept as it is stored (the new stream is rounded to its type anyway), twice
+// unpacked, so that it takes 4 registers per 8 values of bf16.  Measured, 16384 x
+// 4096 bf16, us: residual add and norm 95 (5.6 TB/s), with both norms and a gate
+// 107, codes alone 56 (bound by instructions, 20 per value); with twice the values
+// per thread 100, 130 and 63 (registers), with 512 threads per row, whose next row
+// was loaded early, 88, 144 and 87 (a row's fixed work).
+// BRANCH, POST, CODES: b, w_post and xq are given.
+template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_rows_kernel(const NormParams p) {
     pdl_trigger();
     constexpr int NW = TPR / 32;
     __shared__ float red[TPR > 32 ? 2 : 1][TPR > 32 ? 2 * NW : 1], red_post[TPR > 32 ? NW : 1];
     const int tid = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = TPR == 32 ? (int64_t)gridDim.x * 8 : gridDim.x;
+    const int64_t step = TPR == 32 ? (int64_t)gridDim.x * 4 : gridDim.x;
     const int ng = p.d / 8;
     const float rd = 1.0f / (float)p.d;
-    int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
     pdl_wait();
-    Raw8<BF16> nx[G], nb[BRANCH ? G : 1];
-    auto fetch = [&](int64_t r) {
-        if (r >= p.T) return;
+    int turn = 0;
+    for (int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x; row < p.T; row += step, turn ^= 1) {
+        Raw8<BF16> r[G], b[BRANCH ? G : 1];
+        float gt = 1.0f, rb = 1.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g)
             if (tid + TPR * g < ng) {
-                if (p.x) nx[g].load(p.x, r * p.ldx + (tid + TPR * g) * 8);
-                if (BRANCH) nb[g].load(p.b, r * p.ldb + (tid + TPR * g) * 8);
+                const int at = (tid + TPR * g) * 8;
+                if (BRANCH) b[g].load(p.b, row * p.ldb + at);
+                if (p.x) r[g].load(p.x, row * p.ldx + at);
             }
-    };
-    fetch(row);
-    for (int turn = 0; row < p.T; row += step, turn ^= 1) {   // the same number of rows for every thread of a row
-        float r[G][8], b[BRANCH ? G : 1][8];
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if (p.x) {
-                nx[g].get(r[g]);
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) r[g][c] = 0.0f;
-            }
-            if (BRANCH) nb[g].get(b[g]);
-        }
-        fetch(row + step);
-        if (BRANCH) {
-            float rb = 1.0f;
-            if (POST) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int g = 0; g < G; ++g)
-                    if (tid + TPR * g < ng)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) ss = fmaf(b[g][c], b[g][c], ss);
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if constexpr (TPR > 32) {
-                    if (lane == 0) red_post[warp] = ss;
-                    __syncthreads();
-                    ss = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) ss += red_post[w];
-                }
-                rb = __frsqrt_rn(ss * rd + p.eps);
-            }
-            float gt = 1.0f;
-            if (GATED && p.gate_kind == MOE_GATE_TOKEN) gt = gate_value(p, reinterpret_cast<const float*>(p.gate)[row]);
+        if (BRANCH && p.gate_kind == MOE_GATE_TOKEN) gt = gate_value(p, reinterpret_cast<const float*>(p.gate)[row]);
+        if (POST) {
+            Pair sum(0.0f, 0.0f);
 #pragma unroll
             for (int g = 0; g < G; ++g)
                 if (tid + TPR * g < ng) {
-                    const int at = (tid + TPR * g) * 8;
+                    Pair v[4];
+                    b[g].get(v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
+                }
+            float s0, s1;
+            sum.get(s0, s1);
+            float ss = warp_sum_f(s0 + s1);
+            if constexpr (TPR > 32) {
+                if (lane == 0) red_post[warp] = ss;
+                __syncthreads();
+                ss = warp_sum_f(lane < NW ? red_post[lane] : 0.0f);
+            }
+            rb = __frsqrt_rn(ss * rd + p.eps);
+        }
+        // the new stream, as it is kept; its sum of squares and, for the codes, the
+        // largest value of r (w_pre + offset) inv_s
+        Pair sum(0.0f, 0.0f);
+        float big = 0.0f;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            if (tid + TPR * g < ng) {
+                const int at = (tid + TPR * g) * 8;
+                Pair v[4];
+                if (p.x) {
+                    r[g].get(v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = Pair(p.residual_scale, p.residual_scale) * v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = Pair(0.0f, 0.0f);
+                }
+                if (BRANCH) {
+                    Pair u[4];
+                    b[g].get(u);
                     if (POST) {
-                        float w[8];
-                        load_vals<8>(p.w_post, at, MOE_F32, w);
+                        Pair w[4];
+                        load_weights(p.w_post, at, p.weight_offset, w);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) b[g][c] = b[g][c] * rb * (w[c] + p.weight_offset);
+                        for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(rb, rb) * w[i];
                     }
-                    if (GATED && p.gate_kind == MOE_GATE_TOKEN) {
+                    if (p.gate_kind == MOE_GATE_TOKEN) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) b[g][c] *= gt;
-                    } else if (GATED) {
+                        for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(gt, gt);
+                    } else if (p.gate_kind != MOE_GATE_NONE) {
                         float gv[8];
                         if (p.gate_kind == MOE_GATE_CHANNEL)
                             load_vals<8>(p.gate, at, MOE_F32, gv);
                         else
                             load_vals<8>(p.gate, row * p.ldg + at, p.in_dtype, gv);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) b[g][c] *= gate_value(p, gv[c]);
+                        for (int i = 0; i < 4; ++i)
+                            u[i] = u[i] * Pair(gate_value(p, gv[2 * i]), gate_value(p, gv[2 * i + 1]));
                     }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        r[g][c] = __fadd_rn(__fmul_rn(p.residual_scale, r[g][c]), __fmul_rn(p.branch_scale, b[g][c]));
+                    for (int i = 0; i < 4; ++i) v[i] = v[i] + Pair(p.branch_scale, p.branch_scale) * u[i];
                 }
-        } else if (p.residual_scale != 1.0f) {
+                r[g].set(v);
+                if (p.x_out) r[g].store(p.x_out, row * p.ldxo + at);
+                if (BF16) r[g].get(v);
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-#pragma unroll
-                for (int c = 0; c < 8; ++c) r[g][c] = __fmul_rn(p.residual_scale, r[g][c]);
-        }
-        // the new stream, as it is kept; then v = r (w_pre + offset), its sum of squares and,
-        // for the codes, the largest smoothed value
-        float ss = 0.0f;
-        uint32_t mx = 0;
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) {
-                const int at = (tid + TPR * g) * 8;
-                if (BRANCH || p.residual_scale != 1.0f) round_vals<8>(p.res_dtype, r[g]);
-                if (p.x_out) store_vals<8>(p.x_out, row * p.ldxo + at, p.res_dtype, r[g]);
-                if (p.w_pre) {
-                    float w[8];
-                    load_vals<8>(p.w_pre, at, MOE_F32, w);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        ss = fmaf(r[g][c], r[g][c], ss);
-                        r[g][c] = __fmul_rn(r[g][c], __fadd_rn(w[c], p.weight_offset));
-                    }
-                }
+                for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
                 if (CODES) {
-                    float w[8];
-                    if (p.inv_s) load_vals<8>(p.inv_s, at, MOE_F32, w);
+                    Pair w[4];
+                    if (p.w_pre) {
+                        load_weights(p.w_pre, at, p.weight_offset, w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        mx = max(mx, __float_as_uint(fabsf(p.inv_s ? __fmul_rn(r[g][c], w[c]) : r[g][c])));
+                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
+                    }
+                    if (p.inv_s) {
+                        load_weights(p.inv_s, at, 0.0f, w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float a, c;
+                        v[i].get(a, c);
+                        big = max_abs_nan(max_abs_nan(big, a), c);
+                    }
                 }
             }
         if (!p.w_pre && !CODES) continue;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (CODES) mx = __reduce_max_sync(0xffffffffu, mx);
+        float s0, s1;
+        sum.get(s0, s1);
+        float ss = p.w_pre ? warp_sum_f(s0 + s1) : 0.0f;
+        uint32_t mx = CODES ? __reduce_max_sync(0xffffffffu, __float_as_uint(big)) : 0u;
         if constexpr (TPR > 32) {
             // (the buffer of two rows ago: everybody has read it before the last row's barrier)
             if (lane == 0) {
                 red[turn][warp] = ss;
-                red[turn][NW + warp] = __uint_as_float(mx);
+                if (CODES) red[turn][NW + warp] = __uint_as_float(mx);
             }
             __syncthreads();
-            ss = 0.0f;
-            mx = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                ss += red[turn][w];
-                if (CODES) mx = max(mx, __float_as_uint(red[turn][NW + w]));
-            }
+            if (p.w_pre) ss = warp_sum_f(lane < NW ? red[turn][lane] : 0.0f);
+            if (CODES) mx = __reduce_max_sync(0xffffffffu, lane < NW ? __float_as_uint(red[turn][NW + lane]) : 0u);
         }
         const float rs = p.w_pre ? __frsqrt_rn(ss * rd + p.eps) : 1.0f;
         // codes: a row that holds an infinity or a NaN gets codes 0 and the scale NaN
@@ -444,24 +521,40 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, TPR == 32 ? 4 : 1024 / 
         const float s = CODES && finite ? __fdiv_rn(__uint_as_float(mx), 127.0f) : 0.0f;
         const float inv = CODES && s > 0.0f ? __frcp_rn(s) : 0.0f;
         if (CODES && tid == 0) p.sx[row] = finite ? __fmul_rn(s, rs) : __int_as_float(0x7fc00000);
+        if (!CODES && !p.n_out) continue;
 #pragma unroll
         for (int g = 0; g < G; ++g)
             if (tid + TPR * g < ng) {
                 const int at = (tid + TPR * g) * 8;
-                if (CODES) {
-                    float v[8];
-                    if (p.inv_s) load_vals<8>(p.inv_s, at, MOE_F32, v);
+                Pair v[4], w[4];
+                r[g].get(v);
+                if (p.w_pre) {
+                    load_weights(p.w_pre, at, p.weight_offset, w);
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = p.inv_s ? __fmul_rn(r[g][c], v[c]) : r[g][c];
-                    *reinterpret_cast<uint2*>(p.xq + row * p.ldq + at) =
-                        s > 0.0f ? make_uint2(int8_codes4(v[0], v[1], v[2], v[3], s, inv),
-                                              int8_codes4(v[4], v[5], v[6], v[7], s, inv))
-                                 : make_uint2(0u, 0u);
+                    for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
                 }
                 if (p.n_out) {
+                    Pair n[4];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) r[g][c] *= rs;
-                    store_vals<8>(p.n_out, row * p.ldn + at, p.out_dtype, r[g]);
+                    for (int i = 0; i < 4; ++i) n[i] = v[i] * Pair(rs, rs);
+                    if (p.out_dtype == MOE_BF16) {
+                        Raw8<true> o;
+                        o.set(n);
+                        o.store(p.n_out, row * p.ldn + at);
+                    } else {
+                        Raw8<false> o;
+                        o.set(n);
+                        o.store(p.n_out, row * p.ldn + at);
+                    }
+                }
+                if (CODES) {
+                    if (p.inv_s) {
+                        load_weights(p.inv_s, at, 0.0f, w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
+                    }
+                    *reinterpret_cast<uint2*>(p.xq + row * p.ldq + at) =
+                        s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
                 }
             }
     }
@@ -473,10 +566,10 @@ cudaError_t run(const NormParams& p, cudaStream_t s) {
     return launch_pdl(block_norm_kernel<TPR, G, W>, dim3((unsigned)blocks), dim3(TPR == 32 ? 256 : TPR), 0, s, p);
 }
 
-template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool GATED, bool CODES>
+template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
 cudaError_t run_rows_as(const NormParams& p, cudaStream_t s) {
-    auto kern = block_norm_rows_kernel<TPR, G, BF16, BRANCH, POST, GATED, CODES>;
-    constexpr int kThreads = TPR == 32 ? 256 : TPR;
+    auto kern = block_norm_rows_kernel<TPR, G, BF16, BRANCH, POST, CODES>;
+    constexpr int kThreads = TPR == 32 ? 128 : TPR;
     // as many blocks as can be resident, by device
     static std::atomic<int> resident[64];
     int dev = 0;
@@ -491,41 +584,39 @@ cudaError_t run_rows_as(const NormParams& p, cudaStream_t s) {
         most = per_sm > 0 ? per_sm * sms : sms;
         resident[dev & 63].store(most, std::memory_order_relaxed);
     }
-    const int64_t blocks = TPR == 32 ? (p.T + 7) / 8 : p.T;
+    const int64_t blocks = TPR == 32 ? (p.T + 3) / 4 : p.T;
     return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, s, p);
 }
 
-template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool GATED>
+template <int TPR, int G, bool BF16, bool BRANCH, bool POST>
 cudaError_t run_rows_codes(const NormParams& p, cudaStream_t s) {
-    return p.xq ? run_rows_as<TPR, G, BF16, BRANCH, POST, GATED, true>(p, s)
-                : run_rows_as<TPR, G, BF16, BRANCH, POST, GATED, false>(p, s);
+    return p.xq ? run_rows_as<TPR, G, BF16, BRANCH, POST, true>(p, s) : run_rows_as<TPR, G, BF16, BRANCH, POST, false>(p, s);
 }
 
 template <int TPR, int G, bool BF16>
 cudaError_t run_rows(const NormParams& p, cudaStream_t s) {
-    const bool gated = p.gate_kind != MOE_GATE_NONE;
-    if (!p.b) return run_rows_codes<TPR, G, BF16, false, false, false>(p, s);
-    if (!p.w_post)
-        return gated ? run_rows_codes<TPR, G, BF16, true, false, true>(p, s)
-                     : run_rows_codes<TPR, G, BF16, true, false, false>(p, s);
-    return gated ? run_rows_codes<TPR, G, BF16, true, true, true>(p, s)
-                 : run_rows_codes<TPR, G, BF16, true, true, false>(p, s);
+    if (!p.b) return run_rows_codes<TPR, G, BF16, false, false>(p, s);
+    return p.w_post ? run_rows_codes<TPR, G, BF16, true, true>(p, s) : run_rows_codes<TPR, G, BF16, true, false>(p, s);
 }
 
 template <bool BF16>
 cudaError_t run_rows_by_size(const NormParams& p, cudaStream_t s) {
     const int d = p.d;
     if (d <= 256) return run_rows<32, 1, BF16>(p, s);
-    if (d <= 1024) return run_rows<128, 1, BF16>(p, s);
-    if (d <= 2048) return run_rows<256, 1, BF16>(p, s);
-    if (d <= 4096) return run_rows<512, 1, BF16>(p, s);
-    if (d <= 8192) return run_rows<1024, 1, BF16>(p, s);
-    return run_rows<1024, 2, BF16>(p, s);
+    if (d <= 512) return run_rows<32, 2, BF16>(p, s);
+    if (d <= 1024) return run_rows<32, 4, BF16>(p, s);
+    if (d <= 2048) return run_rows<64, 4, BF16>(p, s);
+    if (d <= 4096) return run_rows<128, 4, BF16>(p, s);
+    if (d <= 8192) return run_rows<256, 4, BF16>(p, s);
+    return run_rows<512, 4, BF16>(p, s);
 }
 
 bool aligned(const void* p, int64_t ld, size_t esz) {
     return !p || (((uintptr_t)p & 15) == 0 && (ld * (int64_t)esz) % 16 == 0);
 }
+
+// Rows from which few threads per row do better.
+constexpr int64_t kManyRows = 600;
 
 }  // namespace
 
@@ -539,14 +630,14 @@ cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
                      (p.gate_kind != MOE_GATE_CHANNEL || aligned(p.gate, 0, 4));
     const int d = p.d;
     if (vec) {
-        const bool both = p.b && p.x;
         const int type = p.x ? p.res_dtype : p.in_dtype;
-        if (!both || p.in_dtype == p.res_dtype)
+        if (p.T >= kManyRows && (!p.b || !p.x || p.in_dtype == p.res_dtype))
             return type == MOE_BF16 ? run_rows_by_size<true>(p, s) : run_rows_by_size<false>(p, s);
-        // a stream and a branch of different types
         if (d <= 512) return run<32, 2, 8>(p, s);
+        if (d <= 1024) return run<128, 1, 8>(p, s);
         if (d <= 2048) return run<256, 1, 8>(p, s);
-        if (d <= 8192) return run<512, 2, 8>(p, s);
+        if (d <= 4096) return run<512, 1, 8>(p, s);
+        if (d <= 8192) return run<1024, 1, 8>(p, s);
         return run<1024, 2, 8>(p, s);
     }
     if (d <= 256) return run<32, 8, 1>(p, s);
