@@ -170,7 +170,7 @@ struct SmallCtl {
     uint32_t tmem_base;
     int abort;
     uint32_t amax[kSmallWarps][kLinearQuantTokens];   // QUANT: the warps' largest values (bits), then ...
-    float scale[kLinearQuantTokens];                  // ... the tokens' scales
+    float scale[128];                                 // the tokens' scales
 };
 
 template <int TN, bool QUANT>
@@ -343,7 +343,18 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
         }
     }
     __syncwarp();
+    // what the output needs besides the sums, while these are formed: four neighbouring
+    // channels per thread where whole words can be stored, else every 32nd, so that a
+    // warp's stores are neighbours
+    const int n0 = nt * kTile + (p.vec ? lane * 4 : lane), dn = p.vec ? 1 : 32;
+    float sw[4], bs[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        sw[c] = p.sw[n0 + c * dn];
+        bs[c] = p.bias ? p.bias[n0 + c * dn] : 0.0f;
+    }
     pdl_wait();
+    if (!QUANT && threadIdx.x < tn) ctl->scale[threadIdx.x] = p.sx[t0 + threadIdx.x];
     const bool ok = nkb == 0 || mbar_wait(&ctl->acc, 0, abort, p.status, 4, 0);
     __syncthreads();   // the stages are free: every copy and MMA is done
     tc_fence_after();
@@ -374,44 +385,45 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
     }
     if (S > 1) cl.sync();
-    // this block's part of the tokens; four channels per thread
+    // this block's part of the tokens
     const int r0 = tn * rank / S, r1 = tn * (rank + 1) / S;
-    const int c4 = lane * 4, n0 = nt * kTile + c4;
-    const float4 sw = *reinterpret_cast<const float4*>(p.sw + n0);
-    const float4 bs = p.bias ? *reinterpret_cast<const float4*>(p.bias + n0) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int r = r0 + warp; r < r1; r += kSmallWarps) {
-        int4 a = make_int4(0, 0, 0, 0);
+        int acc[4] = {0, 0, 0, 0};
         for (int b = 0; b < S; ++b) {
-            const int4 q = *reinterpret_cast<const int4*>(cl.map_shared_rank(part, b) + r * kTile + c4);
-            a.x += q.x, a.y += q.y, a.z += q.z, a.w += q.w;
+            const int32_t* from = cl.map_shared_rank(part, b) + r * kTile;
+            if (p.vec) {
+                const int4 q = reinterpret_cast<const int4*>(from)[lane];
+                acc[0] += q.x, acc[1] += q.y, acc[2] += q.z, acc[3] += q.w;
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[c] += from[lane + 32 * c];
+            }
         }
         const int64_t t = t0 + r;
-        const float sx = QUANT ? ctl->scale[r] : p.sx[t];
-        const float y0 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.x), sx), sw.x), bs.x);
-        const float y1 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.y), sx), sw.y), bs.y);
-        const float y2 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.z), sx), sw.z), bs.z);
-        const float y3 = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(a.w), sx), sw.w), bs.w);
+        const float sx = ctl->scale[r];
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc[c]), sx), sw[c]), bs[c]);
         if (p.out_bf16) {
             uint16_t* dst = reinterpret_cast<uint16_t*>(p.y) + t * p.ldy + n0;
             if (p.vec && n0 + 4 <= p.n) {
                 *reinterpret_cast<uint2*>(dst) = make_uint2(
-                    (uint32_t)f32_to_bf16_bits(y0) | ((uint32_t)f32_to_bf16_bits(y1) << 16),
-                    (uint32_t)f32_to_bf16_bits(y2) | ((uint32_t)f32_to_bf16_bits(y3) << 16));
+                    (uint32_t)f32_to_bf16_bits(y[0]) | ((uint32_t)f32_to_bf16_bits(y[1]) << 16),
+                    (uint32_t)f32_to_bf16_bits(y[2]) | ((uint32_t)f32_to_bf16_bits(y[3]) << 16));
             } else {
-                if (n0 < p.n) dst[0] = f32_to_bf16_bits(y0);
-                if (n0 + 1 < p.n) dst[1] = f32_to_bf16_bits(y1);
-                if (n0 + 2 < p.n) dst[2] = f32_to_bf16_bits(y2);
-                if (n0 + 3 < p.n) dst[3] = f32_to_bf16_bits(y3);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n0 + c * dn < p.n) dst[c * dn] = f32_to_bf16_bits(y[c]);
             }
         } else {
             float* dst = reinterpret_cast<float*>(p.y) + t * p.ldy + n0;
             if (p.vec && n0 + 4 <= p.n) {
-                *reinterpret_cast<float4*>(dst) = make_float4(y0, y1, y2, y3);
+                *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
             } else {
-                if (n0 < p.n) dst[0] = y0;
-                if (n0 + 1 < p.n) dst[1] = y1;
-                if (n0 + 2 < p.n) dst[2] = y2;
-                if (n0 + 3 < p.n) dst[3] = y3;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n0 + c * dn < p.n) dst[c * dn] = y[c];
             }
         }
     }
@@ -616,8 +628,8 @@ bool make_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld
 
 template <int TN, bool QUANT>
 cudaError_t launch_small_as(const LinearTiles& t, const CUtensorMap& tx, LinearParams& p, int split, cudaStream_t s) {
-    // the ring: what the block reads, four stages at most (fewer where two blocks would
-    // not fit on an SM: 64 x 4096 x 32000 took 25.3 us with four, 34.6 with six)
+    // the ring: what the block reads, four stages at most, fewer where two blocks would
+    // not fit on an SM (64 x 4096 x 32000 took 25.3 us with four, 34.6 with six)
     const int nkb = (t.kb + split - 1) / split;
     p.stages = std::min(nkb, kSmallMaxStages);
     while (p.stages > 2 && small_smem<TN, QUANT>(p.stages, nkb) > kSmallMaxSmem / 2) --p.stages;
@@ -629,8 +641,9 @@ cudaError_t launch_small_as(const LinearTiles& t, const CUtensorMap& tx, LinearP
     return launch_cluster(linear_small_kernel<TN, QUANT>, grid, dim3(kSmallThreads), split, smem, s, t.tm_w, tx, p);
 }
 
-cudaError_t launch_small(const LinearTiles& t, const CUtensorMap& tx, LinearParams& p, int tn, int split, cudaStream_t s) {
-    switch (tn) {
+cudaError_t launch_small(const LinearTiles& t, const CUtensorMap& tx, LinearParams& p, int tokens, int split,
+                         cudaStream_t s) {
+    switch (tokens) {
         case 16: return launch_small_as<16, false>(t, tx, p, split, s);
         case 32: return launch_small_as<32, false>(t, tx, p, split, s);
         case 64: return launch_small_as<64, false>(t, tx, p, split, s);
@@ -696,20 +709,44 @@ cudaError_t launch_linear_untile(const LinearTiles& t, int8_t* wq, cudaStream_t 
 
 namespace {
 
-int small_tokens(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+// How a call runs: tokens per block and parts of the inputs for the kernel of a few
+// tokens, or (tokens = 0) the pair kernel.
+struct LinearPlan {
+    int tokens, split;
+};
 
-// Split the inputs while the blocks are at most two per SM (three on two SMs from
-// 64 tokens up), four input tiles each at least.  (A block takes in 50 GB/s at
-// most, so all SMs have to read; past two blocks per SM the rest waits for a second
-// round.  Device time of one call from codes, us, split by 1, 2, 4, 8: 1 x 4096 x
-// 4096 13.1, 8.5, 5.9, 5.6; 32 x 4096 x 6144 14.3, 9.4, 7.2, 12.1; 64 x 4096 x 4096
-// 16.0, 10.7, 7.9, 8.6; 64 x 4096 x 32000 25.3, 32.4, 40.3, 64.1.)
-int small_split(const LinearTiles& t, int T, int tn) {
-    const int64_t blocks = (int64_t)((t.n + kTile - 1) / kTile) * ((T + tn - 1) / tn);
-    const int64_t most = tn <= 32 ? 2 * t.num_sms : t.num_sms + t.num_sms / 2;
-    int split = 1;
-    while (split < kSmallMaxSplit && blocks * split * 2 <= most && t.kb / (split * 2) >= 4) split *= 2;
-    return split;
+// The plan that a model of the kernels' times, in ns, finds the shortest.  A block
+// of the small kernel takes a fixed time that grows with its tokens (its set-up and
+// its output), 700 more if the inputs are split (two cluster barriers), and 350 per
+// input tile (16 KB at the 50 GB/s that a block takes in), 420 where two blocks
+// share an SM; more than two per SM wait for another round.  A pair of SMs takes 8
+// us and 450 ns per input tile and round.  The measured times that the numbers come
+// from (us, model in brackets): 517 x 1000 x 1111 with 32 tokens per block 6.8 (7.2),
+// with 64 in two parts 7.2 (7.4), with 128 11.0 (10.3); 256 x 4096 x 4096 with 64 in
+// two parts 12.1 (12.4), with 128 in four 11.7 (11.6), in two 13.6 (13.8); 1024 x
+// 4096 x 4096 with 128 20.6 (20.9); 32 x 4096 x 6144 with 32 in four parts 7.2
+// (7.9); 4096 x 4096 x 4096 on pairs 63 to 77 (66).
+LinearPlan linear_plan(const LinearTiles& t, int T, bool quantize) {
+    LinearPlan best{0, 1};
+    const int64_t channels = (t.n + kTile - 1) / kTile;
+    const int64_t pairs = (int64_t)((t.n + 255) / 256) * ((T + 255) / 256), at_once = std::max(1, t.num_sms / 2);
+    int64_t least = quantize || T <= 64 ? INT64_MAX : 8000 + (pairs + at_once - 1) / at_once * t.kb * 450;
+    const int fixed[4] = {3800, 3800, 5000, 7500};
+    for (int i = 0; i < 4; ++i) {
+        const int tokens = 16 << i;
+        if ((quantize && tokens > 16) || (i > 0 && tokens / 2 >= T)) break;
+        for (int split = 1; split <= kSmallMaxSplit && (split == 1 || t.kb / split >= 4); split *= 2) {
+            const int64_t blocks = channels * ((T + tokens - 1) / tokens) * split;
+            const int64_t rounds = (blocks + 2 * t.num_sms - 1) / (2 * t.num_sms);
+            const int64_t tiles = (t.kb + split - 1) / split;
+            const int64_t ns = rounds * (fixed[i] + (split > 1 ? 700 : 0) + tiles * (blocks > t.num_sms ? 420 : 350));
+            if (ns < least) {
+                least = ns;
+                best = LinearPlan{tokens, split};
+            }
+        }
+    }
+    return best;
 }
 
 LinearParams linear_params(const LinearTiles& t, int T, void* y, int64_t ldy, int out_dtype) {
@@ -735,7 +772,7 @@ LinearParams linear_params(const LinearTiles& t, int T, void* y, int64_t ldy, in
 bool linear_quantizes(const LinearTiles& t, const void* x, int64_t ldx, int T, int in_dtype) {
     const int64_t esz = in_dtype == MOE_BF16 ? 2 : 4;
     if (t.k % 8 || ((uintptr_t)x & 15) || (ldx * esz) % 16 || T > kLinearQuantTokens) return false;
-    const int split = small_split(t, T, 16), nkb = (t.kb + split - 1) / split;
+    const int split = linear_plan(t, T, true).split, nkb = (t.kb + split - 1) / split;
     return T * nkb * (kTile / 8) <= kOwnGroups * kSmallThreads;   // the part's values fit the threads' registers
 }
 
@@ -746,29 +783,27 @@ cudaError_t launch_linear_quantizing(const LinearTiles& t, const void* x, int64_
     p.ldx = ldx;
     p.in_dtype = in_dtype;
     p.inv_s = inv_s;
-    return launch_small_as<16, true>(t, t.tm_w, p, small_split(t, T, 16), s);   // (no map of x)
+    return launch_small_as<16, true>(t, t.tm_w, p, linear_plan(t, T, true).split, s);   // (no map of x)
 }
 
 cudaError_t launch_linear(const LinearTiles& t, const int8_t* xq, int64_t ldq, const float* sx, int T, void* y, int64_t ldy,
                           int out_dtype, cudaStream_t s) {
     LinearParams p = linear_params(t, T, y, ldy, out_dtype);
     p.sx = sx;
-    const int tn = small_tokens(T);
-    const int64_t pair_tiles = (int64_t)p.n_tiles * p.m_tiles;
-    const bool pairs = T > 128 && pair_tiles * 2 >= t.num_sms;
+    const LinearPlan plan = linear_plan(t, T, false);
     CUtensorMap tx;
-    if (!make_codes_map(&tx, xq, t.k, ldq, T, pairs ? kTile : tn)) return cudaErrorInvalidValue;
-    if (pairs) {
+    if (!make_codes_map(&tx, xq, t.k, ldq, T, plan.tokens ? plan.tokens : kTile)) return cudaErrorInvalidValue;
+    if (plan.tokens == 0) {
         static std::atomic<uint64_t> attr{0};
         cudaError_t e = smem_attr_once(linear_pair_kernel, kPSmem, attr);
         if (e != cudaSuccess) return e;
         int nc = 0;
         e = pair_clusters(&nc);
         if (e != cudaSuccess) return e;
-        const int grid = 2 * (int)std::min<int64_t>(nc, pair_tiles);
+        const int grid = 2 * (int)std::min<int64_t>(nc, (int64_t)p.n_tiles * p.m_tiles);
         return launch_pdl(linear_pair_kernel, dim3(grid), dim3(kPThreads), kPSmem, s, t.tm_w, tx, p);
     }
-    return launch_small(t, tx, p, tn, small_split(t, T, tn), s);
+    return launch_small(t, tx, p, plan.tokens, plan.split, s);
 }
 
 }  // namespace moe
