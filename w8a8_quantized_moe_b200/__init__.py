@@ -639,6 +639,9 @@ def moe_w8a8_ep_combine_blocked(w: Weights, o_blocks, T: int, rank_first, block_
 
 # ------------------------------------------------------------------ around the layer
 
+# Every call below looks at each tensor once, in as few steps as the checks allow:
+# at decode sizes a call's kernels take less time than a dozen attribute reads.
+
 def _refuse(t, name, dtype, dev):
     """Why a tensor is not a CUDA tensor of the type on the current device."""
     torch = _torch()
@@ -651,7 +654,10 @@ def _refuse(t, name, dtype, dev):
 
 def _matrix(t, rows, cols, name, dtype, dev):
     """Pointer and row stride of a [>= rows][>= cols] tensor whose rows are contiguous."""
-    if not isinstance(t, _torch().Tensor) or t.get_device() != dev or t.dtype != dtype:
+    try:
+        if t.get_device() != dev or t.dtype != dtype:
+            _refuse(t, name, dtype, dev)
+    except AttributeError:
         _refuse(t, name, dtype, dev)
     shape = t.shape
     if len(shape) != 2 or shape[0] < rows or shape[1] < cols:
@@ -670,7 +676,10 @@ def _vector(t, n, name, dtype, dev):
     """Pointer of a contiguous tensor of at least n values; None stays None."""
     if t is None:
         return None
-    if not isinstance(t, _torch().Tensor) or t.get_device() != dev or t.dtype != dtype:
+    try:
+        if t.get_device() != dev or t.dtype != dtype:
+            _refuse(t, name, dtype, dev)
+    except AttributeError:
         _refuse(t, name, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -690,6 +699,8 @@ class Linear:
         self.handle = handle
         self.cfg = cfg
         self.smooth = smooth
+        self.n, self.k = cfg.n, cfg.k
+        self.x_dtype, self.y_dtype = _act_dtype(cfg.in_dtype), _act_dtype(cfg.out_dtype)
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
@@ -726,23 +737,23 @@ def moe_w8a8_linear_workspace_size(l: Linear, max_tokens: int) -> int:
 
 
 def moe_w8a8_linear_forward(l: Linear, x, T: int, y, workspace, stream=None):
-    c, dev = l.cfg, _device()
     if T == 0:
         return
-    xp, ldx = _matrix(x, T, c.k, "x", _act_dtype(c.in_dtype), dev)
-    yp, ldy = _matrix(y, T, c.n, "y", _act_dtype(c.out_dtype), dev)
-    _check(lib().moe_w8a8_linear_forward(l.handle, xp, ldx, T, yp, ldy, _vector(workspace, 0, "workspace",
-                                                                                workspace.dtype, dev),
-                                         _nbytes(workspace), _stream(stream)), "moe_w8a8_linear_forward")
+    dev = _device()
+    xp, ldx = _matrix(x, T, l.k, "x", l.x_dtype, dev)
+    yp, ldy = _matrix(y, T, l.n, "y", l.y_dtype, dev)
+    wp = _vector(workspace, 0, "workspace", workspace.dtype, dev)
+    _check(lib().moe_w8a8_linear_forward(l.handle, xp, ldx, T, yp, ldy, wp, _nbytes(workspace), _stream(stream)),
+           "moe_w8a8_linear_forward")
 
 
 def moe_w8a8_linear_forward_codes(l: Linear, xq, sx, T: int, y, stream=None):
-    c, dev = l.cfg, _device()
     if T == 0:
         return
-    qp, ldq = _matrix(xq, T, c.k, "xq", _torch().int8, dev)
-    yp, ldy = _matrix(y, T, c.n, "y", _act_dtype(c.out_dtype), dev)
-    _check(lib().moe_w8a8_linear_forward_codes(l.handle, qp, ldq, _vector(sx, T, "sx", _torch().float32, dev), T, yp, ldy,
+    dev, torch = _device(), _torch()
+    qp, ldq = _matrix(xq, T, l.k, "xq", torch.int8, dev)
+    yp, ldy = _matrix(y, T, l.n, "y", l.y_dtype, dev)
+    _check(lib().moe_w8a8_linear_forward_codes(l.handle, qp, ldq, _vector(sx, T, "sx", torch.float32, dev), T, yp, ldy,
                                                _stream(stream)), "moe_w8a8_linear_forward_codes")
 
 
@@ -773,23 +784,34 @@ def moe_w8a8_block_norm(cfg: moe_w8a8_norm_config, T: int, b=None, x=None, gate=
                         inv_s=None, x_out=None, n_out=None, xq=None, sx=None, stream=None):
     if T == 0:
         return
-    dev, d, f32 = _device(), cfg.d, _torch().float32
+    torch = _torch()
+    dev, d, f32 = _device(), cfg.d, torch.float32
     res = _act_dtype(cfg.res_dtype)
-    none = (None, 0)
-    gp, ldg = none
+    io = moe_w8a8_norm_io()
+    if b is not None:
+        io.b, io.ldb = _matrix(b, T, d, "b", _act_dtype(cfg.in_dtype), dev)
+    if x is not None:
+        io.x, io.ldx = _matrix(x, T, d, "x", res, dev)
     if gate is not None:
         if cfg.gate == MOE_GATE_ELEMENT:
-            gp, ldg = _matrix(gate, T, d, "gate", _act_dtype(cfg.in_dtype), dev)
+            io.gate, io.ldg = _matrix(gate, T, d, "gate", _act_dtype(cfg.in_dtype), dev)
         else:
-            gp = _vector(gate, T if cfg.gate == MOE_GATE_TOKEN else d, "gate", f32, dev)
-    io = moe_w8a8_norm_io(
-        *(none if b is None else _matrix(b, T, d, "b", _act_dtype(cfg.in_dtype), dev)),
-        *(none if x is None else _matrix(x, T, d, "x", res, dev)), gp, ldg, _vector(w_post, d, "w_post", f32, dev),
-        _vector(w_pre, d, "w_pre", f32, dev), _vector(inv_s, d, "inv_s", f32, dev),
-        *(none if x_out is None else _matrix(x_out, T, d, "x_out", res, dev)),
-        *(none if n_out is None else _matrix(n_out, T, d, "n_out", _act_dtype(cfg.out_dtype), dev)),
-        *(none if xq is None else _matrix(xq, T, d, "xq", _torch().int8, dev)), _vector(sx, T, "sx", f32, dev))
-    _check(lib().moe_w8a8_block_norm(ctypes.byref(cfg), ctypes.byref(io), T, _stream(stream)), "moe_w8a8_block_norm")
+            io.gate = _vector(gate, T if cfg.gate == MOE_GATE_TOKEN else d, "gate", f32, dev)
+    if w_post is not None:
+        io.w_post = _vector(w_post, d, "w_post", f32, dev)
+    if w_pre is not None:
+        io.w_pre = _vector(w_pre, d, "w_pre", f32, dev)
+    if inv_s is not None:
+        io.inv_s = _vector(inv_s, d, "inv_s", f32, dev)
+    if x_out is not None:
+        io.x_out, io.ldxo = _matrix(x_out, T, d, "x_out", res, dev)
+    if n_out is not None:
+        io.n_out, io.ldn = _matrix(n_out, T, d, "n_out", _act_dtype(cfg.out_dtype), dev)
+    if xq is not None:
+        io.xq, io.ldq = _matrix(xq, T, d, "xq", torch.int8, dev)
+    if sx is not None:
+        io.sx = _vector(sx, T, "sx", f32, dev)
+    _check(lib().moe_w8a8_block_norm(cfg, io, T, _stream(stream)), "moe_w8a8_block_norm")
 
 
 def moe_w8a8_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, allowed=None, prob=None,
@@ -806,7 +828,7 @@ def moe_w8a8_sample(logits, u, token, temperature=None, top_k=None, top_p=None, 
         lp, ld, ap, lda, _vector(temperature, rows, "temperature", f32, dev), _vector(top_k, rows, "top_k", i32, dev),
         _vector(top_p, rows, "top_p", f32, dev), _vector(min_p, rows, "min_p", f32, dev), _vector(u, rows, "u", f32, dev),
         _vector(token, rows, "token", i32, dev), _vector(prob, rows, "prob", f32, dev))
-    _check(lib().moe_w8a8_sample(ctypes.byref(io), rows, vocab, MOE_BF16 if bf16 else MOE_F32,
+    _check(lib().moe_w8a8_sample(io, rows, vocab, MOE_BF16 if bf16 else MOE_F32,
                                  _stream(stream)), "moe_w8a8_sample")
 
 
