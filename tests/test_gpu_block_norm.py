@@ -168,3 +168,21 @@ def test_stream_and_graph(M):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(-want[0], got[0]) and torch.equal(-want[1], got[1])
+
+
+@pytest.mark.parametrize("d", [34, 36, 510, 516, 1002, 1004, 2050, 4002, 4004, 5002, 5004, 16380, 16382])
+@pytest.mark.parametrize("inp,res,out", [("bf16", "bf16", "bf16"), ("f32", "f32", "f32"), ("bf16", "f32", "bf16")])
+def test_rows_on_smaller_boundaries(M, d, inp, res, out):
+    """Widths that divide by 2 or 4 only, and strides that do."""
+    run_case(M, 7, d, inp, res, out, True, "element", True, True, True)
+    run_case(M, 5, d, inp, res, out, False, "none", False, True, False, pad=2)
+    run_case(M, 3, d, inp, res, out, True, "token", False, False, False, pad=1)
+
+
+@pytest.mark.parametrize("T", [1, 7, 8, 9, 199, 200, 201, 2500])
+@pytest.mark.parametrize("d", [40, 256, 512, 520, 1024, 2048, 2560, 4096])
+def test_row_counts(M, T, d):
+    """Both kernels of rows on 16-byte boundaries, at the count where one takes over from the other."""
+    run_case(M, T, d, "bf16", "bf16", "bf16", True, "channel", True, True, True, offset=1.0)
+    run_case(M, T, d, "f32", "f32", "bf16", False, "none", False, True, True)
+    run_case(M, T, d, "bf16", "bf16", "f32", False, "element", False, False, False, pad=8)

@@ -16,24 +16,52 @@
 // many rows on 16-byte boundaries, bound by memory and instructions, with few
 // threads per row; block_norm_kernel for a few rows, bound by latency, with many,
 // and for every type, stride and size.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-// W consecutive values from index i of a row (W = 8: 16-byte accesses).
+// W consecutive values from index i of a row, in one access (W = 8 in fp32: two).
 template <int W>
 __device__ __forceinline__ void load_vals(const void* p, int64_t i, int dtype, float (&v)[W]) {
     if constexpr (W == 8) {
         load8_act(p, i, dtype, v);
+    } else if (dtype == MOE_BF16) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + i;
+        if constexpr (W == 1) {
+            v[0] = bf16_bits_to_f32(*q);
+        } else {
+            uint32_t w[W / 2];
+            if constexpr (W == 4) {
+                const uint2 u = *reinterpret_cast<const uint2*>(q);
+                w[0] = u.x, w[W / 2 - 1] = u.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t*>(q);
+            }
+#pragma unroll
+            for (int c = 0; c < W / 2; ++c) {
+                v[2 * c] = __uint_as_float(w[c] << 16);
+                v[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+            }
+        }
     } else {
-        v[0] = dtype == MOE_BF16 ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p)[i])
-                                 : reinterpret_cast<const float*>(p)[i];
+        const float* q = reinterpret_cast<const float*>(p) + i;
+        if constexpr (W == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(q);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        } else if constexpr (W == 2) {
+            const float2 u = *reinterpret_cast<const float2*>(q);
+            v[0] = u.x, v[1] = u.y;
+        } else {
+            v[0] = *q;
+        }
     }
 }
 
-// Round to the stored type and store; v keeps the rounded values.
+// Round to the stored type; v keeps the rounded values.
 template <int W>
 __device__ __forceinline__ void round_vals(int dtype, float (&v)[W]) {
     if (dtype == MOE_BF16) {
@@ -44,25 +72,35 @@ __device__ __forceinline__ void round_vals(int dtype, float (&v)[W]) {
 
 template <int W>
 __device__ __forceinline__ void store_vals(void* p, int64_t i, int dtype, const float (&v)[W]) {
-    if constexpr (W == 8) {
-        if (dtype == MOE_BF16) {
-            uint32_t w[4];
+    if (dtype == MOE_BF16) {
+        uint16_t* q = reinterpret_cast<uint16_t*>(p) + i;
+        if constexpr (W == 1) {
+            *q = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+            uint32_t w[W / 2];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < W / 2; ++c) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * c], v[2 * c + 1]);
                 w[c] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if constexpr (W == 8)
+                *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+            else if constexpr (W == 4)
+                *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint32_t*>(q) = w[0];
         }
     } else {
-        if (dtype == MOE_BF16)
-            reinterpret_cast<uint16_t*>(p)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-        else
-            reinterpret_cast<float*>(p)[i] = v[0];
+        float* q = reinterpret_cast<float*>(p) + i;
+        if constexpr (W >= 4) {
+#pragma unroll
+            for (int c = 0; c < W; c += 4)
+                reinterpret_cast<float4*>(q)[c / 4] = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        } else if constexpr (W == 2) {
+            *reinterpret_cast<float2*>(q) = make_float2(v[0], v[1]);
+        } else {
+            *q = v[0];
+        }
     }
 }
 
@@ -172,9 +210,12 @@ __device__ __forceinline__ uint2 int8_codes8(const Pair (&v)[4], float s, float 
 
 // TPR threads per row, each with G groups of W values: group g of thread t is
 // values [(t + TPR g) W, ... + W).  Rows per block: 8 when a warp owns a row,
-// else one.
-template <int TPR, int G, int W>
+// else one.  TYPE: the one type of the branch, the stream and n_out, or -1 (each
+// as the parameters say).
+template <int TPR, int G, int W, int TYPE>
 __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const NormParams p) {
+    const int in_dtype = TYPE < 0 ? p.in_dtype : TYPE, res_dtype = TYPE < 0 ? p.res_dtype : TYPE,
+              out_dtype = TYPE < 0 ? p.out_dtype : TYPE;
     pdl_trigger();
     __shared__ float red[2][TPR > 32 ? 2 * TPR / 32 : 2];
     const int tid = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x;
@@ -186,7 +227,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
     if (p.x) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) load_vals<W>(p.x, row * p.ldx + (int64_t)(tid + TPR * g) * W, p.res_dtype, r[g]);
+            if (tid + TPR * g < ng) load_vals<W>(p.x, row * p.ldx + (int64_t)(tid + TPR * g) * W, res_dtype, r[g]);
     } else {
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -196,7 +237,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
     if (p.b) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) load_vals<W>(p.b, row * p.ldb + (int64_t)(tid + TPR * g) * W, p.in_dtype, b[g]);
+            if (tid + TPR * g < ng) load_vals<W>(p.b, row * p.ldb + (int64_t)(tid + TPR * g) * W, in_dtype, b[g]);
     }
     uint32_t mx = 0;
     if (p.b) {
@@ -233,7 +274,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
                     if (p.gate_kind == MOE_GATE_CHANNEL)
                         load_vals<W>(p.gate, at, MOE_F32, gv);
                     else
-                        load_vals<W>(p.gate, row * p.ldg + at, p.in_dtype, gv);
+                        load_vals<W>(p.gate, row * p.ldg + at, in_dtype, gv);
                     if (p.gate_sigmoid) {
 #pragma unroll
                         for (int c = 0; c < W; ++c) gv[c] = 1.0f / (1.0f + expf(-gv[c]));
@@ -258,8 +299,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
     for (int g = 0; g < G; ++g)
         if (tid + TPR * g < ng) {
             const int64_t at = (int64_t)(tid + TPR * g) * W;
-            round_vals<W>(p.res_dtype, r[g]);
-            if (p.x_out) store_vals<W>(p.x_out, row * p.ldxo + at, p.res_dtype, r[g]);
+            round_vals<W>(res_dtype, r[g]);
+            if (p.x_out) store_vals<W>(p.x_out, row * p.ldxo + at, res_dtype, r[g]);
             if (p.w_pre) {
                 float w[W];
                 load_vals<W>(p.w_pre, at, MOE_F32, w);
@@ -298,13 +339,23 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
                     const Pair v[4] = {Pair(b[g][0], b[g][1]), Pair(b[g][2], b[g][3]), Pair(b[g][4], b[g][5]), Pair(b[g][6], b[g][7])};
                     *reinterpret_cast<uint2*>(dst) = s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
                 } else {
-                    *dst = s > 0.0f ? (int8_t)quant_code_fast(b[g][0], s, inv) : (int8_t)0;
+                    uint32_t q = 0;
+                    if (s > 0.0f) {
+#pragma unroll
+                        for (int c = 0; c < W; ++c) q |= ((uint32_t)quant_code_fast(b[g][c], s, inv) & 0xffu) << (8 * c);
+                    }
+                    if constexpr (W == 4)
+                        *reinterpret_cast<uint32_t*>(dst) = q;
+                    else if constexpr (W == 2)
+                        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)q;
+                    else
+                        *dst = (int8_t)q;
                 }
             }
             if (p.n_out) {
 #pragma unroll
                 for (int c = 0; c < W; ++c) r[g][c] *= rs;
-                store_vals<W>(p.n_out, row * p.ldn + at, p.out_dtype, r[g]);
+                store_vals<W>(p.n_out, row * p.ldn + at, out_dtype, r[g]);
             }
         }
 }
@@ -560,10 +611,17 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_rows_kernel(
     }
 }
 
+template <int TPR, int G, int W, int TYPE>
+cudaError_t run_as(const NormParams& p, cudaStream_t s) {
+    const int64_t blocks = TPR == 32 ? (p.T + 7) / 8 : p.T;
+    return launch_pdl(block_norm_kernel<TPR, G, W, TYPE>, dim3((unsigned)blocks), dim3(TPR == 32 ? 256 : TPR), 0, s, p);
+}
+
 template <int TPR, int G, int W>
 cudaError_t run(const NormParams& p, cudaStream_t s) {
-    const int64_t blocks = TPR == 32 ? (p.T + 7) / 8 : p.T;
-    return launch_pdl(block_norm_kernel<TPR, G, W>, dim3((unsigned)blocks), dim3(TPR == 32 ? 256 : TPR), 0, s, p);
+    const int type = p.x ? p.res_dtype : p.in_dtype;
+    if ((p.b && p.in_dtype != type) || (p.n_out && p.out_dtype != type)) return run_as<TPR, G, W, -1>(p, s);
+    return type == MOE_BF16 ? run_as<TPR, G, W, MOE_BF16>(p, s) : run_as<TPR, G, W, MOE_F32>(p, s);
 }
 
 template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
@@ -611,8 +669,20 @@ cudaError_t run_rows_by_size(const NormParams& p, cudaStream_t s) {
     return run_rows<512, 4, BF16>(p, s);
 }
 
-bool aligned(const void* p, int64_t ld, size_t esz) {
-    return !p || (((uintptr_t)p & 15) == 0 && (ld * (int64_t)esz) % 16 == 0);
+// Rows of W values (times the size of one) stay on their boundaries.
+bool aligned(const void* p, int64_t ld, size_t esz, int W) {
+    return !p || (((uintptr_t)p % (esz * W)) == 0 && ld % W == 0);
+}
+
+bool in_groups(const NormParams& p, int W) {
+    auto size = [](int dtype) -> size_t { return dtype == MOE_BF16 ? 2 : 4; };
+    // (fp32 groups of 8 are two accesses of 16 bytes)
+    auto ok = [&](const void* q, int64_t ld, size_t esz) { return aligned(q, ld, esz, std::min(W, (int)(16 / esz))); };
+    return p.d % W == 0 && ok(p.b, p.ldb, size(p.in_dtype)) && ok(p.x, p.ldx, size(p.res_dtype)) &&
+           ok(p.x_out, p.ldxo, size(p.res_dtype)) && ok(p.n_out, p.ldn, size(p.out_dtype)) && ok(p.w_post, 0, 4) &&
+           ok(p.w_pre, 0, 4) && ok(p.inv_s, 0, 4) &&
+           (p.gate_kind != MOE_GATE_ELEMENT || ok(p.gate, p.ldg, size(p.in_dtype))) &&
+           (p.gate_kind != MOE_GATE_CHANNEL || ok(p.gate, 0, 4));   // (xq is on 16 bytes with its rows)
 }
 
 // Rows from which few threads per row do better (599 x 8192 with many: 16.9 us, 600 with
@@ -622,15 +692,8 @@ constexpr int64_t kManyRows = 200;
 }  // namespace
 
 cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
-    const size_t eb = p.in_dtype == MOE_BF16 ? 2 : 4, er = p.res_dtype == MOE_BF16 ? 2 : 4,
-                 eo = p.out_dtype == MOE_BF16 ? 2 : 4;
-    const bool vec = p.d % 8 == 0 && aligned(p.b, p.ldb, eb) && aligned(p.x, p.ldx, er) &&
-                     aligned(p.x_out, p.ldxo, er) && aligned(p.n_out, p.ldn, eo) && aligned(p.w_post, 0, 4) &&
-                     aligned(p.w_pre, 0, 4) && aligned(p.inv_s, 0, 4) && aligned(p.xq, p.ldq, 1) &&
-                     (p.gate_kind != MOE_GATE_ELEMENT || aligned(p.gate, p.ldg, eb)) &&
-                     (p.gate_kind != MOE_GATE_CHANNEL || aligned(p.gate, 0, 4));
     const int d = p.d;
-    if (vec) {
+    if (in_groups(p, 8)) {
         const int type = p.x ? p.res_dtype : p.in_dtype;
         if (p.T >= kManyRows && (!p.b || !p.x || p.in_dtype == p.res_dtype))
             return type == MOE_BF16 ? run_rows_by_size<true>(p, s) : run_rows_by_size<false>(p, s);
@@ -640,6 +703,18 @@ cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
         if (d <= 4096) return run<512, 1, 8>(p, s);
         if (d <= 8192) return run<1024, 1, 8>(p, s);
         return run<1024, 2, 8>(p, s);
+    }
+    if (in_groups(p, 4)) {
+        if (d <= 512) return run<32, 4, 4>(p, s);
+        if (d <= 1024) return run<128, 2, 4>(p, s);
+        if (d <= 4096) return run<256, 4, 4>(p, s);
+        return run<1024, 4, 4>(p, s);
+    }
+    if (in_groups(p, 2)) {
+        if (d <= 512) return run<32, 8, 2>(p, s);
+        if (d <= 1024) return run<128, 4, 2>(p, s);
+        if (d <= 4096) return run<512, 4, 2>(p, s);
+        return run<1024, 8, 2>(p, s);
     }
     if (d <= 256) return run<32, 8, 1>(p, s);
     if (d <= 1024) return run<256, 4, 1>(p, s);
