@@ -637,7 +637,7 @@ cudaError_t launch_small_as(const LinearTiles& t, const CUtensorMap& tx, LinearP
     static std::atomic<uint64_t> attr{0};
     cudaError_t e = smem_attr_once(linear_small_kernel<TN, QUANT>, kSmallMaxSmem, attr);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((t.n + kTile - 1) / kTile * split), (unsigned)((p.T + TN - 1) / TN));
+    const dim3 grid((unsigned)((t.n + kTile - 1) / kTile * split), (unsigned)(((int64_t)p.T + TN - 1) / TN));
     return launch_cluster(linear_small_kernel<TN, QUANT>, grid, dim3(kSmallThreads), split, smem, s, t.tm_w, tx, p);
 }
 
@@ -729,14 +729,15 @@ struct LinearPlan {
 LinearPlan linear_plan(const LinearTiles& t, int T, bool quantize) {
     LinearPlan best{0, 1};
     const int64_t channels = (t.n + kTile - 1) / kTile;
-    const int64_t pairs = (int64_t)((t.n + 255) / 256) * ((T + 255) / 256), at_once = std::max(1, t.num_sms / 2);
+    const int64_t pairs = (int64_t)((t.n + 255) / 256) * (((int64_t)T + 255) / 256), at_once = std::max(1, t.num_sms / 2);
     int64_t least = quantize || T <= 64 ? INT64_MAX : 8000 + (pairs + at_once - 1) / at_once * t.kb * 450;
     const int fixed[4] = {3800, 3800, 5000, 7500};
     for (int i = 0; i < 4; ++i) {
         const int tokens = 16 << i;
         if ((quantize && tokens > 16) || (i > 0 && tokens / 2 >= T)) break;
+        if (((int64_t)T + tokens - 1) / tokens > 65535) continue;   // the grid's second dimension
         for (int split = 1; split <= kSmallMaxSplit && (split == 1 || t.kb / split >= 4); split *= 2) {
-            const int64_t blocks = channels * ((T + tokens - 1) / tokens) * split;
+            const int64_t blocks = channels * (((int64_t)T + tokens - 1) / tokens) * split;
             const int64_t rounds = (blocks + 2 * t.num_sms - 1) / (2 * t.num_sms);
             const int64_t tiles = (t.kb + split - 1) / split;
             const int64_t ns = rounds * (fixed[i] + (split > 1 ? 700 : 0) + tiles * (blocks > t.num_sms ? 420 : 350));
@@ -763,7 +764,7 @@ LinearParams linear_params(const LinearTiles& t, int T, void* y, int64_t ldy, in
     p.vec = ((uintptr_t)y & 15) == 0 && (ldy * (p.out_bf16 ? 2 : 4)) % 16 == 0;
     p.status = t.status;
     p.n_tiles = (t.n + 255) / 256;
-    p.m_tiles = (T + 255) / 256;
+    p.m_tiles = (int)(((int64_t)T + 255) / 256);
     return p;
 }
 
