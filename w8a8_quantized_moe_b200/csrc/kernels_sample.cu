@@ -70,11 +70,12 @@ __device__ __forceinline__ float minus_inf() { return __uint_as_float(0xff800000
 // Where |max c| is too large for k_l, l - max takes the place of l; it is exact
 // for every token whose mass is not far below the smallest unit.
 struct Softmax {
-    float shift, c, c32, c_lo, rm, t_max;   // t_max: kMagic + k_m
+    float max_logit, shift, c, c32, c_lo, rm, t_max;   // t_max: kMagic + k_m
     double m, cd;
     const uint32_t* tab;                    // shared: round(2^(30 + j / 32))
-    __device__ __forceinline__ void init(float max_logit, float temperature, const uint32_t* table) {
-        m = (double)max_logit;
+    __device__ __forceinline__ void init(float largest, float temperature, const uint32_t* table) {
+        max_logit = largest;
+        m = (double)largest;
         cd = 1.4426950408889634074 / (double)temperature;
         c = (float)cd;
         c_lo = (float)(cd - (double)c);
@@ -100,6 +101,34 @@ struct Softmax {
         const int q = __float2int_rn(__fmul_rn(p, 4294967296.0f));
         return T + (uint32_t)(int)(((int64_t)(uint64_t)T * q) >> 32);
     }
+    // The places and mantissas of four tokens, by pairs of operations.
+    __device__ __forceinline__ void place4(const float4& l, Pair (&lr)[2], Pair (&t)[2]) const {
+        const Pair less(-shift, -shift), scale(c32, c32), magic(kMagic, kMagic);
+        lr[0] = Pair(l.x, l.y) + less;
+        lr[1] = Pair(l.z, l.w) + less;
+        t[0] = fma2(lr[0], scale, magic);
+        t[1] = fma2(lr[1], scale, magic);
+    }
+    __device__ __forceinline__ void mantissa4(const Pair (&lr)[2], const Pair (&t)[2], uint32_t (&M)[4]) const {
+        auto two = [](float v) { return Pair(v, v); };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            Pair r = fma2(lr[i], two(c), (t[i] + two(-kMagic)) * two(-0.03125f));
+            r = fma2(lr[i], two(c_lo), r) + two(-rm);
+            Pair p = fma2(r, two(0.00961812910763f), two(0.0555041086648f));
+            p = fma2(p, r, two(0.240226506959f));
+            p = fma2(p, r, two(0.693147180560f));
+            p = p * r * two(4294967296.0f);
+            float q[2], at[2];
+            p.get(q[0], q[1]);
+            t[i].get(at[0], at[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t T = tab[(__float_as_int(at[j]) - __float_as_int(t_max)) & 31];
+                M[2 * i + j] = T + (uint32_t)(int)(((int64_t)(uint64_t)T * __float2int_rn(q[j])) >> 32);
+            }
+        }
+    }
     // in units of 2^-45, for a token `below` places under the largest
     static __device__ __forceinline__ uint64_t fixed(uint32_t M, int below) {
         return ((uint64_t)M << (kMassBits - 30)) >> ((below + 31) >> 5);
@@ -112,7 +141,7 @@ struct Softmax {
     // the mass as a fraction of the largest, to 2^-21
     __device__ __forceinline__ float approximate(float l) const {
         float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(__fsub_rn(l, (float)m), c)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(__fsub_rn(l, max_logit), c)));
         return e;
     }
     // the mass in 64 bits, for the chosen token's probability
@@ -622,7 +651,7 @@ __device__ __forceinline__ uint64_t bin_value(const uint32_t* h, int bin) {
 
 // The bin at which the running count (or mass) of the row reaches `need`, and
 // what lies above it; kMassBins when it does not.  `own`: this thread's part of
-// the row's mass, whose sum is `total`; need is top_p of it, or given.  Two
+// the mass that is in no bin; `total`: all of it.  need is top_p of it, or given.  Two
 // levels, so that a block reads 64 words of each other one's shared memory: the
 // sums over powers of two, then the 32 bins of one of them.
 template <bool MASS>
@@ -646,6 +675,7 @@ __device__ int find_bin(Row& r, uint64_t own, float top_p, double& need, uint64_
         s += r.sh->gather[0][b][r.lane];
         total += r.sh->gather_total[b];
     }
+    total += warp_sum_u64(s);
     if (MASS) need = fmax((double)top_p * (double)total, 1.0);
     uint64_t inc = warp_scan_u64(s, r.lane);
     uint32_t at = __ballot_sync(0xffffffffu, (double)inc >= need);
@@ -669,9 +699,8 @@ __device__ int find_bin(Row& r, uint64_t own, float top_p, double& need, uint64_
     return g * 32 + j;
 }
 
-__device__ __forceinline__ float clean(float v, bool allowed) {
-    return allowed && v == v ? __fadd_rn(v, 0.0f) : minus_inf();
-}
+// A logit as it is kept: -0 as +0, a NaN or what may not be chosen as -infinity.
+__device__ __forceinline__ float clean(float v) { return __fadd_rn(fmaxf(v, minus_inf()), 0.0f); }
 
 __device__ __forceinline__ uint64_t kept_mass(const Row& r, const Softmax& sm, const Cut& cut, int i) {
     const float l = r.logits[i];
@@ -760,11 +789,15 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
                                       : reinterpret_cast<const float*>(p.logits)[base + g * 8 + c])
                                : minus_inf();
             }
-            const int i0 = r.lo + g * 8;   // a multiple of 8
-            const uint32_t bits = allowed ? allowed[i0 >> 5] >> (i0 & 31) : 0xffu;
+            if (allowed) {
+                const int i0 = r.lo + g * 8;   // a multiple of 8
+                const uint32_t bits = allowed[i0 >> 5] >> (i0 & 31);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] = (bits >> c) & 1u ? v[c] : minus_inf();
+            }
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                v[c] = clean(v[c], (bits >> c) & 1u);
+                v[c] = clean(v[c]);
                 own_max = fmaxf(own_max, v[c]);
             }
             reinterpret_cast<float4*>(r.logits)[2 * g] = make_float4(v[0], v[1], v[2], v[3]);
@@ -775,7 +808,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         for (int i = r.tid; i < r.n; i += kSaThreads) {
             const float v = p.dtype == MOE_BF16 ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(p.logits)[base + i])
                                                 : reinterpret_cast<const float*>(p.logits)[base + i];
-            r.logits[i] = clean(v, !allowed || ((allowed[(r.lo + i) >> 5] >> ((r.lo + i) & 31)) & 1u));
+            const bool may = !allowed || ((allowed[(r.lo + i) >> 5] >> ((r.lo + i) & 31)) & 1u);
+            r.logits[i] = may ? clean(v) : minus_inf();
             own_max = fmaxf(own_max, r.logits[i]);
         }
         if (r.tid < (-r.n & 3)) r.logits[r.n + r.tid] = minus_inf();
@@ -854,26 +888,37 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         // tail <= 1 - top_p together, so the prefix ends above them
         const float tail = log2f(fminf(1.0f - top_p, 0.015625f) / (float)p.vocab) - 0.5f;
         const float t_last = sm.t_max - fminf(fmaxf(floorf(-32.0f * tail), 0.0f), (float)(kMassBins - 1));
-        uint64_t z = 0;
         float zt = 0.0f;   // the tail's part, less than 1/64 in all, by the approximate 2^x
-        for (int i = r.tid * 4; i < r.n; i += kSaThreads * 4) {
-            const float4 q = *reinterpret_cast<const float4*>(r.logits + i);
-            const float l[4] = {q.x, q.y, q.z, q.w};
+        const int steps = (r.n + kSaThreads * 4 - 1) / (kSaThreads * 4);
+        for (int k = 0; k < steps; ++k) {   // whole warps: the vote below
+            const int i = (k * kSaThreads + r.tid) * 4;
+            const float4 l = i < r.n ? *reinterpret_cast<const float4*>(r.logits + i)
+                                     : make_float4(minus_inf(), minus_inf(), minus_inf(), minus_inf());
+            Pair lr[2], at[2];
+            sm.place4(l, lr, at);
+            float t[4];
+            at[0].get(t[0], t[1]);
+            at[1].get(t[2], t[3]);
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+            if (__any_sync(0xffffffffu, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) >= t_last)) {
+                uint32_t M[4];
+                sm.mantissa4(lr, at, M);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float t = sm.place(l[j]);
-                if (t >= t_last) {
-                    const uint32_t M = sm.mantissa(l[j], t);
-                    const int bin = sm.bin(t);
-                    z += max(Softmax::fixed(M, bin), (uint64_t)1);
-                    atomicAdd(&r.hist[bin], M & 0xffffu);
-                    atomicAdd(&r.hist[kMassBins + bin], M >> 16);
-                } else {
-                    zt += sm.approximate(l[j]);
+                for (int j = 0; j < 4; ++j) {
+                    if (t[j] >= t_last) {
+                        const int bin = sm.bin(t[j]);
+                        atomicAdd(&r.hist[bin], M[j] & 0xffffu);
+                        atomicAdd(&r.hist[kMassBins + bin], M[j] >> 16);
+                    } else {
+                        zt += sm.approximate(lv[j]);
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) zt += sm.approximate(lv[j]);
             }
         }
-        z += (uint64_t)((double)zt * (double)(1ull << kMassBits));
+        const uint64_t z = (uint64_t)((double)zt * (double)(1ull << kMassBits));
         uint64_t total = 0, above = 0;
         double need = 0.0;
         const int b = find_bin<true>(r, z, top_p, need, total, above);
