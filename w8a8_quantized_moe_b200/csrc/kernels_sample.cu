@@ -18,8 +18,8 @@
 //     the threads' largest tokens, which bounds the top_k from below, or of all
 //     tokens that the top_p could reach, with their masses) names the bin where
 //     a prefix ends.
-//   - If the tokens down to that bin are few, the first block of the cluster
-//     gets them as a list and finishes the row alone.
+//   - If the tokens down to that bin are few (2048), the first block of the
+//     cluster gets them as a list and finishes the row alone.
 //   - Else it gets the tokens of that bin alone and finds the cut inside; the
 //     blocks then add up what lies above the cut, in the order of the tokens.
 //   - Where a bin holds more than a list takes (many equal logits), the cut is
@@ -167,7 +167,7 @@ struct SaShared {
     uint64_t warp_sum[kSaWarps];
     uint64_t coarse[32], total;           // this block's histogram by powers of two, and its mass
     uint64_t gather[2][kSaMaxCluster][32], gather_total[kSaMaxCluster];
-    uint64_t found_above;
+    uint64_t found_above, found_entry;
     uint64_t block_above[kSaMaxCluster];  // in the first block: each block's mass over the bin of the cut
     uint64_t pick_target, pick_total;
     int32_t pick_block;
@@ -552,10 +552,107 @@ template <bool BY_INDEX>
 __device__ __forceinline__ void order_list(Row& r, const Softmax& sm, uint64_t* list, uint64_t* run, int n) {
     if (n <= kCounted)
         order_by_count<BY_INDEX>(r, sm, list, run, n);
-    else if (n <= kSaThreads)
-        order_by_sort<1, BY_INDEX>(r, sm, list, run, n);
     else
-        order_by_sort<kList / kSaThreads, BY_INDEX>(r, sm, list, run, n);
+        order_by_sort<1, BY_INDEX>(r, sm, list, run, n);
+}
+
+// In a longer list no order is formed.  Among the entries e[0 .. n) that are at
+// least `least`, in falling order: the one at which the running value (their
+// masses, or with COUNT their number) reaches `need`, at most the sum of all.  By
+// one block; e and mass lie in its shared memory.  Each round spreads the range
+// that is left over 512 bins, until one holds at most 32 entries (they are
+// distinct).
+template <bool COUNT>
+__device__ __noinline__ uint64_t select_entry(Row& r, const uint64_t* e, const uint64_t* mass, int n, uint64_t least,
+                                              uint64_t need) {
+    uint64_t* bins = reinterpret_cast<uint64_t*>(r.hist);
+    uint32_t* counts = r.hist + 2 * kSaThreads;
+    uint64_t* few = r.sh->gather[0][0];   // up to 32 entries, then their values
+    uint64_t lo = least, hi = ~(uint64_t)0, above = 0;
+    uint32_t left = (uint32_t)n;
+    bool ranged = false;
+    while (left > 32) {
+        if (!ranged) {   // the smallest and largest high words
+            uint32_t k0 = 0xffffffffu, k1 = 0;
+            for (int i = r.tid; i < n; i += kSaThreads)
+                if (e[i] >= least) {
+                    k0 = min(k0, (uint32_t)(e[i] >> 32));
+                    k1 = max(k1, (uint32_t)(e[i] >> 32));
+                }
+            k0 = __reduce_min_sync(0xffffffffu, k0);
+            k1 = __reduce_max_sync(0xffffffffu, k1);
+            __syncthreads();
+            if (r.lane == 0) r.sh->warp_sum[r.warp] = ((uint64_t)k1 << 32) | k0;
+            __syncthreads();
+            const uint64_t w = r.sh->warp_sum[r.lane % kSaWarps];
+            lo = max(lo, (uint64_t)__reduce_min_sync(0xffffffffu, (uint32_t)w) << 32);
+            hi = ((uint64_t)__reduce_max_sync(0xffffffffu, (uint32_t)(w >> 32)) << 32) | 0xffffffffu;
+            ranged = true;
+        }
+        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 9);
+        bins[r.tid] = 0;
+        counts[r.tid] = 0;
+        __syncthreads();
+        for (int i = r.tid; i < n; i += kSaThreads) {
+            const uint64_t x = e[i];
+            if (x < lo || x > hi) continue;
+            const int b = (int)((hi - x) >> shift);
+            atomicAdd(&counts[b], 1u);
+            if (!COUNT) atomicAdd((unsigned long long*)&bins[b], (unsigned long long)mass[i]);
+        }
+        __syncthreads();
+        const uint64_t v = COUNT ? counts[r.tid] : bins[r.tid];
+        uint64_t all;
+        const uint64_t inc = above + r.block_scan(v, all);
+        if (inc - v < need && inc >= need) {
+            r.sh->found = (uint32_t)r.tid;
+            r.sh->found_above = inc - v;
+        }
+        __syncthreads();
+        const uint32_t b = r.sh->found;
+        above = r.sh->found_above;
+        left = counts[b];
+        hi -= (uint64_t)b << shift;
+        lo = max(lo, hi - (((uint64_t)1 << shift) - 1));
+        __syncthreads();
+    }
+    if (r.tid == 0) r.sh->own_count = 0;
+    __syncthreads();
+    for (int i = r.tid; i < n; i += kSaThreads)
+        if (e[i] >= lo && e[i] <= hi) {
+            const uint32_t at = atomicAdd(&r.sh->own_count, 1u);
+            few[at] = e[i];
+            few[32 + at] = COUNT ? 1 : mass[i];
+        }
+    __syncthreads();
+    if (r.warp == 0) {
+        const int c = (int)r.sh->own_count;
+        const uint64_t mine = r.lane < c ? few[r.lane] : 0;
+        uint64_t before = above;
+#pragma unroll 4
+        for (int j = 0; j < c; ++j) before += few[j] > mine ? few[32 + j] : 0;
+        if (r.lane < c && before < need && before + few[32 + r.lane] >= need) r.sh->found_entry = mine;
+    }
+    __syncthreads();
+    return r.sh->found_entry;
+}
+
+// The masses of the list's n entries, to the first half of the scratch.
+__device__ void list_masses(Row& r, const Softmax& sm, const uint64_t* list, uint64_t* mass, int n) {
+    for (int i = r.tid; i < n; i += kSaThreads) mass[i] = sm.mass(entry_logit(list[i]));
+    __syncthreads();
+}
+
+// The mass of the entries that are at least `least`.
+__device__ uint64_t mass_from(Row& r, const uint64_t* e, const uint64_t* mass, int n, uint64_t least) {
+    uint64_t s = 0;
+    for (int i = r.tid; i < n; i += kSaThreads) s += e[i] >= least ? mass[i] : 0;
+    return r.block_sum(s);
+}
+
+// The whole number that a sum of masses reaches when it reaches `need`, at most `total`.
+__device__ __forceinline__ uint64_t whole_need(double need, uint64_t total) {
+    return min((uint64_t)fmax(ceil(need), 1.0), total);
 }
 
 // The first of n places where `at` holds (it holds from there on), by one warp;
@@ -593,6 +690,30 @@ __device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, in
                             double need, float min_logit) {
     uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
     uint64_t* list = run + kList;
+    if (n > kSaThreads) {
+        uint64_t* mass = run;
+        list_masses(r, sm, list, mass, n);
+        uint64_t least = 0;
+        if (top_k > 0 && top_k < n) least = select_entry<true>(r, list, mass, n, 0, (uint64_t)top_k);
+        if (top_p < 1.0f) {
+            const uint64_t z = mass_from(r, list, mass, n, least);
+            if (top_k > 0) need = (double)top_p * (double)z;
+            least = select_entry<false>(r, list, mass, n, least, whole_need(need, z));
+        }
+        least = max(least, (uint64_t)key_of(min_logit) << 32);
+        uint64_t kept = 0;
+        for (int i = r.tid; i < n; i += kSaThreads) {
+            const uint64_t e = list[i];
+            const bool in = e >= least;
+            kept += in ? mass[i] : 0;
+            list[i] = in ? (e << 32) | (e >> 32) : 0;   // ~index on top: it falls as the index rises
+        }
+        const uint64_t total = r.block_sum(kept);
+        uint64_t e = select_entry<false>(r, list, mass, n, 1, target_of(p.u[row], total) + 1);
+        e = (e << 32) | (e >> 32);
+        if (r.tid == 0) choose(p, sm, row, entry_index(e), entry_logit(e), total);
+        return;
+    }
     order_list<false>(r, sm, list, run, n);
     if (top_k > 0) n = min(n, top_k);
     if (top_p < 1.0f) {
@@ -617,12 +738,27 @@ __device__ void finish_list(Row& r, const SampleParams& p, const Softmax& sm, in
 __device__ void cut_in_list(Row& r, const SampleParams& p, const Softmax& sm, int row, int n, uint64_t above, double need) {
     uint64_t* run = reinterpret_cast<uint64_t*>(r.scratch);
     uint64_t* list = run + kList;
-    order_list<false>(r, sm, list, run, n);
-    const int last = min(n - 1, first_where(n, r.lane, [&](int i) { return (double)(above + run[i]) >= need; }));
-    for (int i = r.tid; i <= last; i += kSaThreads)
-        atomicAdd((unsigned long long*)&r.sh->block_above[entry_index(list[i]) / p.per_block],
-                  (unsigned long long)(run[i] - (i ? run[i - 1] : 0)));
-    const uint64_t total = above + run[last];
+    uint64_t last, total;
+    if (n <= kCounted) {
+        order_list<false>(r, sm, list, run, n);
+        const int at = min(n - 1, first_where(n, r.lane, [&](int i) { return (double)(above + run[i]) >= need; }));
+        for (int i = r.tid; i <= at; i += kSaThreads)
+            atomicAdd((unsigned long long*)&r.sh->block_above[entry_index(list[i]) / p.per_block],
+                      (unsigned long long)(run[i] - (i ? run[i - 1] : 0)));
+        last = list[at];
+        total = above + run[at];
+    } else {
+        list_masses(r, sm, list, run, n);
+        last = select_entry<false>(r, list, run, n, 0, whole_need(need - (double)above, mass_from(r, list, run, n, 0)));
+        uint64_t kept = 0;
+        for (int i = r.tid; i < n; i += kSaThreads)
+            if (list[i] >= last) {
+                kept += run[i];
+                atomicAdd((unsigned long long*)&r.sh->block_above[entry_index(list[i]) / p.per_block],
+                          (unsigned long long)run[i]);
+            }
+        total = above + r.block_sum(kept);
+    }
     const uint64_t target = target_of(p.u[row], total);
     __syncthreads();
     if (r.tid < r.nb) {
@@ -630,8 +766,8 @@ __device__ void cut_in_list(Row& r, const SampleParams& p, const Softmax& sm, in
         int b = 0;
         while (b + 1 < r.nb && before + r.sh->block_above[b] <= target) before += r.sh->block_above[b++];
         SaShared* to = r.cl.map_shared_rank(r.sh, r.tid);
-        to->cut_value = entry_logit(list[last]);
-        to->cut_index = entry_index(list[last]) + 1;
+        to->cut_value = entry_logit(last);
+        to->cut_index = entry_index(last) + 1;
         to->pick_block = b;
         to->pick_target = target - before;
         to->pick_total = total;
