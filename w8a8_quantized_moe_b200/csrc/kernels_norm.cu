@@ -413,178 +413,186 @@ __device__ __forceinline__ float gate_value(const NormParams& p, float g) {
 // row's fixed work (two reductions, a division) is shared by many values; the row
 // is kept as it is stored (the new stream is rounded to its type anyway), twice
 // unpacked, so that it takes 4 registers per 8 values of bf16.  Measured, 16384 x
-// 4096 bf16, us: residual add and norm 95 (5.6 TB/s), with both norms and a gate
-// 107, codes alone 56 (bound by instructions, 20 per value); with twice the values
-// per thread 100, 130 and 63 (registers), with 512 threads per row, whose next row
-// was loaded early, 88, 144 and 87 (a row's fixed work).
+// 4096 bf16, us: residual add and norm 81 (6.6 TB/s), with both norms and a gate
+// 95, codes alone 52 (bound by instructions, 20 per value); blocks that stay and
+// take every n-th row 97, 101 and 56; twice the values per thread 100, 130 and 63
+// (registers); 512 threads per row, the next row's loads early, 88, 144 and 87 (a
+// row's fixed work).
 // BRANCH, POST, CODES: b, w_post and xq are given.
 template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_rows_kernel(const NormParams p) {
     pdl_trigger();
     constexpr int NW = TPR / 32;
-    __shared__ float red[TPR > 32 ? 2 : 1][TPR > 32 ? 2 * NW : 1], red_post[TPR > 32 ? NW : 1];
+    __shared__ float red[TPR > 32 ? 2 * NW : 1], red_post[TPR > 32 ? NW : 1];
     const int tid = TPR == 32 ? (threadIdx.x & 31) : threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = TPR == 32 ? (int64_t)gridDim.x * 4 : gridDim.x;
+    const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x;
     const int ng = p.d / 8;
     const float rd = 1.0f / (float)p.d;
     pdl_wait();
-    int turn = 0;
-    for (int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + warp : blockIdx.x; row < p.T; row += step, turn ^= 1) {
-        Raw8<BF16> r[G], b[BRANCH ? G : 1];
-        float gt = 1.0f, rb = 1.0f;
+    if (row >= p.T) return;   // a whole warp, or nobody
+    Raw8<BF16> r[G], b[BRANCH ? G : 1];
+    float gt = 1.0f, rb = 1.0f;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) {
-                const int at = (tid + TPR * g) * 8;
-                if (BRANCH) b[g].load(p.b, row * p.ldb + at);
-                if (p.x) r[g].load(p.x, row * p.ldx + at);
-            }
-        if (BRANCH && p.gate_kind == MOE_GATE_TOKEN) gt = gate_value(p, reinterpret_cast<const float*>(p.gate)[row]);
-        if (POST) {
-            Pair sum(0.0f, 0.0f);
-#pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (tid + TPR * g < ng) {
-                    Pair v[4];
-                    b[g].get(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
-                }
-            float s0, s1;
-            sum.get(s0, s1);
-            float ss = warp_sum_f(s0 + s1);
-            if constexpr (TPR > 32) {
-                if (lane == 0) red_post[warp] = ss;
-                __syncthreads();
-                ss = warp_sum_f(lane < NW ? red_post[lane] : 0.0f);
-            }
-            rb = __frsqrt_rn(ss * rd + p.eps);
+    for (int g = 0; g < G; ++g)
+        if (tid + TPR * g < ng) {
+            const int at = (tid + TPR * g) * 8;
+            if (BRANCH) b[g].load(p.b, row * p.ldb + at);
+            if (p.x) r[g].load(p.x, row * p.ldx + at);
         }
-        // the new stream, as it is kept; its sum of squares and, for the codes, the
-        // largest value of r (w_pre + offset) inv_s
+    if (BRANCH && p.gate_kind == MOE_GATE_TOKEN) gt = gate_value(p, reinterpret_cast<const float*>(p.gate)[row]);
+    if (POST) {
         Pair sum(0.0f, 0.0f);
-        float big = 0.0f;
 #pragma unroll
         for (int g = 0; g < G; ++g)
             if (tid + TPR * g < ng) {
-                const int at = (tid + TPR * g) * 8;
                 Pair v[4];
-                if (p.x) {
-                    r[g].get(v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = Pair(p.residual_scale, p.residual_scale) * v[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = Pair(0.0f, 0.0f);
-                }
-                if (BRANCH) {
-                    Pair u[4];
-                    b[g].get(u);
-                    if (POST) {
-                        Pair w[4];
-                        load_weights(p.w_post, at, p.weight_offset, w);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(rb, rb) * w[i];
-                    }
-                    if (p.gate_kind == MOE_GATE_TOKEN) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(gt, gt);
-                    } else if (p.gate_kind != MOE_GATE_NONE) {
-                        float gv[8];
-                        if (p.gate_kind == MOE_GATE_CHANNEL)
-                            load_vals<8>(p.gate, at, MOE_F32, gv);
-                        else
-                            load_vals<8>(p.gate, row * p.ldg + at, p.in_dtype, gv);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            u[i] = u[i] * Pair(gate_value(p, gv[2 * i]), gate_value(p, gv[2 * i + 1]));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = v[i] + Pair(p.branch_scale, p.branch_scale) * u[i];
-                }
-                r[g].set(v);
-                if (p.x_out) r[g].store(p.x_out, row * p.ldxo + at);
-                if (BF16) r[g].get(v);
+                b[g].get(v);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
-                if (CODES) {
-                    Pair w[4];
-                    if (p.w_pre) {
-                        load_weights(p.w_pre, at, p.weight_offset, w);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
-                    }
-                    if (p.inv_s) {
-                        load_weights(p.inv_s, at, 0.0f, w);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float a, c;
-                        v[i].get(a, c);
-                        big = max_abs_nan(max_abs_nan(big, a), c);
-                    }
-                }
             }
-        if (!p.w_pre && !CODES) continue;
         float s0, s1;
         sum.get(s0, s1);
-        float ss = p.w_pre ? warp_sum_f(s0 + s1) : 0.0f;
-        uint32_t mx = CODES ? __reduce_max_sync(0xffffffffu, __float_as_uint(big)) : 0u;
+        float ss = warp_sum_f(s0 + s1);
         if constexpr (TPR > 32) {
-            // (the buffer of two rows ago: everybody has read it before the last row's barrier)
-            if (lane == 0) {
-                red[turn][warp] = ss;
-                if (CODES) red[turn][NW + warp] = __uint_as_float(mx);
-            }
+            if (lane == 0) red_post[warp] = ss;
             __syncthreads();
-            if (p.w_pre) ss = warp_sum_f(lane < NW ? red[turn][lane] : 0.0f);
-            if (CODES) mx = __reduce_max_sync(0xffffffffu, lane < NW ? __float_as_uint(red[turn][NW + lane]) : 0u);
+            ss = warp_sum_f(lane < NW ? red_post[lane] : 0.0f);
         }
-        const float rs = p.w_pre ? __frsqrt_rn(ss * rd + p.eps) : 1.0f;
-        // codes: a row that holds an infinity or a NaN gets codes 0 and the scale NaN
-        const bool finite = mx < 0x7f800000u;
-        const float s = CODES && finite ? __fdiv_rn(__uint_as_float(mx), 127.0f) : 0.0f;
-        const float inv = CODES && s > 0.0f ? __frcp_rn(s) : 0.0f;
-        if (CODES && tid == 0) p.sx[row] = finite ? __fmul_rn(s, rs) : __int_as_float(0x7fc00000);
-        if (!CODES && !p.n_out) continue;
+        rb = __frsqrt_rn(ss * rd + p.eps);
+    }
+    // the new stream, as it is kept; its sum of squares and, for the codes, the
+    // largest value of r (w_pre + offset) inv_s
+    Pair sum(0.0f, 0.0f);
+    float big = 0.0f;
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) {
-                const int at = (tid + TPR * g) * 8;
-                Pair v[4], w[4];
+    for (int g = 0; g < G; ++g)
+        if (tid + TPR * g < ng) {
+            const int at = (tid + TPR * g) * 8;
+            Pair v[4];
+            if (p.x) {
                 r[g].get(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = Pair(p.residual_scale, p.residual_scale) * v[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = Pair(0.0f, 0.0f);
+            }
+            if (BRANCH) {
+                Pair u[4];
+                b[g].get(u);
+                if (POST) {
+                    Pair w[4];
+                    load_weights(p.w_post, at, p.weight_offset, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(rb, rb) * w[i];
+                }
+                if (p.gate_kind == MOE_GATE_TOKEN) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = u[i] * Pair(gt, gt);
+                } else if (p.gate_kind != MOE_GATE_NONE) {
+                    Pair gv[4];
+                    if (p.gate_kind == MOE_GATE_CHANNEL) {
+                        load_weights(reinterpret_cast<const float*>(p.gate), at, 0.0f, gv);
+                    } else {
+                        Raw8<BF16> q;
+                        q.load(p.gate, row * p.ldg + at);
+                        q.get(gv);
+                    }
+                    if (p.gate_sigmoid) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float a, c;
+                            gv[i].get(a, c);
+                            gv[i] = Pair(gate_value(p, a), gate_value(p, c));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[i] = u[i] * gv[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = v[i] + Pair(p.branch_scale, p.branch_scale) * u[i];
+            }
+            r[g].set(v);
+            if (p.x_out) r[g].store(p.x_out, row * p.ldxo + at);
+            if (BF16) r[g].get(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
+            if (CODES) {
+                Pair w[4];
                 if (p.w_pre) {
                     load_weights(p.w_pre, at, p.weight_offset, w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
                 }
-                if (p.n_out) {
-                    Pair n[4];
+                if (p.inv_s) {
+                    load_weights(p.inv_s, at, 0.0f, w);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) n[i] = v[i] * Pair(rs, rs);
-                    if (p.out_dtype == MOE_BF16) {
-                        Raw8<true> o;
-                        o.set(n);
-                        o.store(p.n_out, row * p.ldn + at);
-                    } else {
-                        Raw8<false> o;
-                        o.set(n);
-                        o.store(p.n_out, row * p.ldn + at);
-                    }
+                    for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
                 }
-                if (CODES) {
-                    if (p.inv_s) {
-                        load_weights(p.inv_s, at, 0.0f, w);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
-                    }
-                    *reinterpret_cast<uint2*>(p.xq + row * p.ldq + at) =
-                        s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
+                for (int i = 0; i < 4; ++i) {
+                    float a, c;
+                    v[i].get(a, c);
+                    big = max_abs_nan(max_abs_nan(big, a), c);
                 }
             }
+        }
+    if (!p.w_pre && !CODES) return;
+    float s0, s1;
+    sum.get(s0, s1);
+    float ss = p.w_pre ? warp_sum_f(s0 + s1) : 0.0f;
+    uint32_t mx = CODES ? __reduce_max_sync(0xffffffffu, __float_as_uint(big)) : 0u;
+    if constexpr (TPR > 32) {
+        if (lane == 0) {
+            red[warp] = ss;
+            if (CODES) red[NW + warp] = __uint_as_float(mx);
+        }
+        __syncthreads();
+        if (p.w_pre) ss = warp_sum_f(lane < NW ? red[lane] : 0.0f);
+        if (CODES) mx = __reduce_max_sync(0xffffffffu, lane < NW ? __float_as_uint(red[NW + lane]) : 0u);
     }
+    const float rs = p.w_pre ? __frsqrt_rn(ss * rd + p.eps) : 1.0f;
+    // codes: a row that holds an infinity or a NaN gets codes 0 and the scale NaN
+    const bool finite = mx < 0x7f800000u;
+    const float s = CODES && finite ? __fdiv_rn(__uint_as_float(mx), 127.0f) : 0.0f;
+    const float inv = CODES && s > 0.0f ? __frcp_rn(s) : 0.0f;
+    if (CODES && tid == 0) p.sx[row] = finite ? __fmul_rn(s, rs) : __int_as_float(0x7fc00000);
+    if (!CODES && !p.n_out) return;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        if (tid + TPR * g < ng) {
+            const int at = (tid + TPR * g) * 8;
+            Pair v[4], w[4];
+            r[g].get(v);
+            if (p.w_pre) {
+                load_weights(p.w_pre, at, p.weight_offset, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
+            }
+            if (p.n_out) {
+                Pair n[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) n[i] = v[i] * Pair(rs, rs);
+                if (p.out_dtype == MOE_BF16) {
+                    Raw8<true> o;
+                    o.set(n);
+                    o.store(p.n_out, row * p.ldn + at);
+                } else {
+                    Raw8<false> o;
+                    o.set(n);
+                    o.store(p.n_out, row * p.ldn + at);
+                }
+            }
+            if (CODES) {
+                if (p.inv_s) {
+                    load_weights(p.inv_s, at, 0.0f, w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = v[i] * w[i];
+                }
+                *reinterpret_cast<uint2*>(p.xq + row * p.ldq + at) =
+                    s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
+            }
+        }
 }
 
 template <int TPR, int G, int W, int TYPE>
@@ -604,22 +612,8 @@ template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
 cudaError_t run_rows_as(const NormParams& p, cudaStream_t s) {
     auto kern = block_norm_rows_kernel<TPR, G, BF16, BRANCH, POST, CODES>;
     constexpr int kThreads = TPR == 32 ? 128 : TPR;
-    // as many blocks as can be resident, by device
-    static std::atomic<int> resident[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    int most = resident[dev & 63].load(std::memory_order_relaxed);
-    if (most == 0) {
-        int per_sm = 0, sms = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, 0);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) return e;
-        most = per_sm > 0 ? per_sm * sms : sms;
-        resident[dev & 63].store(most, std::memory_order_relaxed);
-    }
     const int64_t blocks = TPR == 32 ? (p.T + 3) / 4 : p.T;
-    return launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, s, p);
+    return launch_pdl(kern, dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
 }
 
 template <int TPR, int G, bool BF16, bool BRANCH, bool POST>
