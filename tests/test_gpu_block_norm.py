@@ -186,3 +186,26 @@ def test_row_counts(M, T, d):
     run_case(M, T, d, "bf16", "bf16", "bf16", True, "channel", True, True, True, offset=1.0)
     run_case(M, T, d, "f32", "f32", "bf16", False, "none", False, True, True)
     run_case(M, T, d, "bf16", "bf16", "f32", False, "element", False, False, False, pad=8)
+
+
+@pytest.mark.parametrize("T", [3, 250])
+@pytest.mark.parametrize("d", [512, 516, 1001])
+@pytest.mark.parametrize("inp,res", [("bf16", "f32"), ("f32", "bf16")])
+def test_branch_without_a_stream_of_another_type(M, T, d, inp, res):
+    """No x: the new stream still has its own type, which x_out and the norm's input are rounded to."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + d)
+    code = {"f32": M.MOE_F32, "bf16": M.MOE_BF16}
+    b = torch.randn(T, d, generator=g, device="cuda").to(DT[inp])
+    w = torch.rand(d, generator=g, device="cuda") + 0.5
+    x_out = torch.full((T + 1, d), 9.0, dtype=DT[res], device="cuda")
+    n_out = torch.full((T + 1, d), 9.0, device="cuda")
+    xq, sx = torch.empty(T, (d + 15) // 16 * 16, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    M.moe_w8a8_block_norm(M.make_norm_config(d, code[inp], code[res], M.MOE_F32), T, b=b, w_pre=w, x_out=x_out, n_out=n_out,
+                          xq=xq, sx=sx)
+    assert torch.equal(x_out[:T], b.float().to(DT[res])) and (x_out[T] == 9).all() and (n_out[T] == 9).all()
+    r = host(x_out[:T])
+    n = r / R.rms(r, np.float64(np.float32(1e-6))) * host(w)
+    assert (np.abs(host(n_out[:T]) - n) <= 1.01 * (RMS_U + 4 * U32) * np.abs(n) + 1e-37).all()
+    q, _ = R.quantize_rows(r.astype(np.float32) * host(w).astype(np.float32))
+    assert np.array_equal(xq[:, :d].cpu().numpy(), q)

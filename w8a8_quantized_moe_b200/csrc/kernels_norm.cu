@@ -603,7 +603,7 @@ cudaError_t run_as(const NormParams& p, cudaStream_t s) {
 
 template <int TPR, int G, int W>
 cudaError_t run(const NormParams& p, cudaStream_t s) {
-    const int type = p.x ? p.res_dtype : p.in_dtype;
+    const int type = p.res_dtype;   // the new stream's, also where there is no x
     if ((p.b && p.in_dtype != type) || (p.n_out && p.out_dtype != type)) return run_as<TPR, G, W, -1>(p, s);
     return type == MOE_BF16 ? run_as<TPR, G, W, MOE_BF16>(p, s) : run_as<TPR, G, W, MOE_F32>(p, s);
 }
@@ -664,9 +664,8 @@ constexpr int64_t kManyRows = 200;
 cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
     const int d = p.d;
     if (in_groups(p, 8)) {
-        const int type = p.x ? p.res_dtype : p.in_dtype;
-        if (p.T >= kManyRows && (!p.b || !p.x || p.in_dtype == p.res_dtype))
-            return type == MOE_BF16 ? run_rows_by_size<true>(p, s) : run_rows_by_size<false>(p, s);
+        if (p.T >= kManyRows && (!p.b || p.in_dtype == p.res_dtype))
+            return p.res_dtype == MOE_BF16 ? run_rows_by_size<true>(p, s) : run_rows_by_size<false>(p, s);
         if (d <= 512) return run<32, 2, 8>(p, s);
         if (d <= 1024) return run<128, 1, 8>(p, s);
         if (d <= 2048) return run<256, 1, 8>(p, s);
