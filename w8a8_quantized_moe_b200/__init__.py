@@ -260,8 +260,15 @@ def _host_ptr(a, name="array", allow_none=False):
     raise TypeError(f"{name} must be a contiguous host array")
 
 
+_cuda_ready = False
+
+
 def _stream(stream):
     if stream is None:
+        global _cuda_ready
+        if not _cuda_ready:
+            _torch().cuda.init()
+            _cuda_ready = True
         c = _torch()._C
         return c._cuda_getCurrentRawStream(c._cuda_getDevice())
     if isinstance(stream, int):
