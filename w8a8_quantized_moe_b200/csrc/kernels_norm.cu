@@ -184,12 +184,20 @@ __device__ __forceinline__ uint2 int8_codes8(const Pair (&v)[4], float s, float 
     return make_uint2(q[0], q[1]);
 }
 
+__device__ __forceinline__ float gate_value(const NormParams& p, float g) {
+    return p.gate_sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
+}
+
 // TPR threads per row, each with G groups of W values: group g of thread t is
 // values [(t + TPR g) W, ... + W).  Rows per block: 8 when a warp owns a row,
 // else one.  TYPE: the one type of the branch, the stream and n_out, or -1 (each
-// as the parameters say).
+// as the parameters say).  What a call asks for is decided between the passes over
+// a thread's groups, not inside them: with single values (rows off every boundary)
+// a decision per value cost more than the value (16384 x 4095 bf16 with codes and
+// n_out: 320 us, 147 instructions per value; now 231).
 template <int TPR, int G, int W, int TYPE>
-__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, TPR == 32 ? 4 : W == 1 && TPR < 1024 ? 1536 / TPR : 1024 / TPR)
+    block_norm_kernel(const NormParams p) {
     const int in_dtype = TYPE < 0 ? p.in_dtype : TYPE, res_dtype = TYPE < 0 ? p.res_dtype : TYPE,
               out_dtype = TYPE < 0 ? p.out_dtype : TYPE;
     pdl_trigger();
@@ -200,69 +208,83 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
     if (row >= p.T) return;   // a whole warp, or nobody
     const int ng = p.d / W;
     float r[G][W], b[G][W];
-    if (p.x) {
+    // f(group, index of its first value) for the thread's groups.  Past the row's end a
+    // group stands for the row's last one when it loads and holds zeros, so that the
+    // passes between loads and stores are free of branches.
+    auto all = [&](auto f) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) f(g, min((tid + TPR * g) * W, p.d - W));
+    };
+    auto each = [&](auto f) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) load_vals<W>(p.x, row * p.ldx + (int64_t)(tid + TPR * g) * W, res_dtype, r[g]);
+            if (tid + TPR * g < ng) f(g, (tid + TPR * g) * W);
+    };
+    auto load = [&](float (&v)[G][W], const void* from, int64_t ld, int dtype) {
+        all([&](int g, int at) {
+            load_vals<W>(from, row * ld + at, dtype, v[g]);
+            if (tid + TPR * g >= ng) {
+#pragma unroll
+                for (int c = 0; c < W; ++c) v[g][c] = 0.0f;
+            }
+        });
+    };
+    auto times = [&](float (&v)[G][W], const float* weights, float offset) {
+        all([&](int g, int at) {
+            float w[W];
+            load_vals<W>(weights, at, MOE_F32, w);
+#pragma unroll
+            for (int c = 0; c < W; ++c) v[g][c] = __fmul_rn(v[g][c], offset != 0.0f ? __fadd_rn(w[c], offset) : w[c]);
+        });
+    };
+    if (p.x) {
+        load(r, p.x, p.ldx, res_dtype);
     } else {
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
             for (int c = 0; c < W; ++c) r[g][c] = 0.0f;
     }
-    if (p.b) {
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) load_vals<W>(p.b, row * p.ldb + (int64_t)(tid + TPR * g) * W, in_dtype, b[g]);
-    }
+    if (p.b) load(b, p.b, p.ldb, in_dtype);
     uint32_t mx = 0;
     if (p.b) {
-        float scale = p.branch_scale;
         if (p.w_post) {
             float ss = 0.0f;
+            all([&](int g, int) {
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (tid + TPR * g < ng)
-#pragma unroll
-                    for (int c = 0; c < W; ++c) ss = fmaf(b[g][c], b[g][c], ss);
+                for (int c = 0; c < W; ++c) ss = fmaf(b[g][c], b[g][c], ss);
+            });
             row_reduce<TPR>(ss, mx, red[0]);
             const float rb = __frsqrt_rn(ss / (float)p.d + p.eps);
+            all([&](int g, int) {
 #pragma unroll
-            for (int g = 0; g < G; ++g)
-                if (tid + TPR * g < ng) {
-                    float w[W];
-                    load_vals<W>(p.w_post, (int64_t)(tid + TPR * g) * W, MOE_F32, w);
-#pragma unroll
-                    for (int c = 0; c < W; ++c) b[g][c] = b[g][c] * rb * (w[c] + p.weight_offset);
-                }
+                for (int c = 0; c < W; ++c) b[g][c] *= rb;
+            });
+            times(b, p.w_post, p.weight_offset);
         }
-        float gt = 1.0f;
         if (p.gate_kind == MOE_GATE_TOKEN) {
-            gt = reinterpret_cast<const float*>(p.gate)[row];
-            if (p.gate_sigmoid) gt = 1.0f / (1.0f + expf(-gt));
-        }
+            const float gt = gate_value(p, reinterpret_cast<const float*>(p.gate)[row]);
+            all([&](int g, int) {
 #pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tid + TPR * g < ng) {
-                const int64_t at = (int64_t)(tid + TPR * g) * W;
+                for (int c = 0; c < W; ++c) b[g][c] *= gt;
+            });
+        } else if (p.gate_kind != MOE_GATE_NONE) {
+            const bool element = p.gate_kind == MOE_GATE_ELEMENT;
+            all([&](int g, int at) {
                 float gv[W];
-                if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_ELEMENT) {
-                    if (p.gate_kind == MOE_GATE_CHANNEL)
-                        load_vals<W>(p.gate, at, MOE_F32, gv);
-                    else
-                        load_vals<W>(p.gate, row * p.ldg + at, in_dtype, gv);
-                    if (p.gate_sigmoid) {
+                if (element)
+                    load_vals<W>(p.gate, row * p.ldg + at, in_dtype, gv);
+                else
+                    load_vals<W>(p.gate, at, MOE_F32, gv);
 #pragma unroll
-                        for (int c = 0; c < W; ++c) gv[c] = 1.0f / (1.0f + expf(-gv[c]));
-                    }
-                } else {
+                for (int c = 0; c < W; ++c) b[g][c] *= gate_value(p, gv[c]);
+            });
+        }
+        all([&](int g, int) {
 #pragma unroll
-                    for (int c = 0; c < W; ++c) gv[c] = gt;
-                }
-#pragma unroll
-                for (int c = 0; c < W; ++c)
-                    r[g][c] = __fadd_rn(__fmul_rn(p.residual_scale, r[g][c]), __fmul_rn(scale, b[g][c] * gv[c]));
-            }
+            for (int c = 0; c < W; ++c)
+                r[g][c] = __fadd_rn(__fmul_rn(p.residual_scale, r[g][c]), __fmul_rn(p.branch_scale, b[g][c]));
+        });
     } else if (p.residual_scale != 1.0f) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -270,70 +292,89 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR) block_norm_kernel(const
             for (int c = 0; c < W; ++c) r[g][c] = __fmul_rn(p.residual_scale, r[g][c]);
     }
     // the new stream, as it is kept; v = r (w_pre + offset) for the norm and, smoothed, for the codes
-    float ss = 0.0f;
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-        if (tid + TPR * g < ng) {
-            const int64_t at = (int64_t)(tid + TPR * g) * W;
-            round_vals<W>(res_dtype, r[g]);
-            if (p.x_out) store_vals<W>(p.x_out, row * p.ldxo + at, res_dtype, r[g]);
-            if (p.w_pre) {
-                float w[W];
-                load_vals<W>(p.w_pre, at, MOE_F32, w);
-#pragma unroll
-                for (int c = 0; c < W; ++c) {
-                    ss = fmaf(r[g][c], r[g][c], ss);
-                    r[g][c] = __fmul_rn(r[g][c], __fadd_rn(w[c], p.weight_offset));
-                }
-            }
-            if (p.xq) {
-                float w[W];
-                if (p.inv_s) load_vals<W>(p.inv_s, at, MOE_F32, w);
-#pragma unroll
-                for (int c = 0; c < W; ++c) {
-                    b[g][c] = p.inv_s ? __fmul_rn(r[g][c], w[c]) : r[g][c];
-                    mx = max(mx, __float_as_uint(fabsf(b[g][c])));
-                }
-            }
-        }
+    all([&](int g, int) { round_vals<W>(res_dtype, r[g]); });
+    if (p.x_out) each([&](int g, int at) { store_vals<W>(p.x_out, row * p.ldxo + at, res_dtype, r[g]); });
     if (!p.w_pre && !p.xq) return;
-    mx = p.xq ? mx : 0u;
+    float ss = 0.0f, big = 0.0f;
+    if (p.w_pre) {
+        all([&](int g, int) {
+#pragma unroll
+            for (int c = 0; c < W; ++c) ss = fmaf(r[g][c], r[g][c], ss);
+        });
+        times(r, p.w_pre, p.weight_offset);
+    }
+    if (p.xq) {
+        all([&](int g, int) {
+#pragma unroll
+            for (int c = 0; c < W; ++c) b[g][c] = r[g][c];
+        });
+        if (p.inv_s) times(b, p.inv_s, 0.0f);
+        all([&](int g, int) {
+#pragma unroll
+            for (int c = 0; c < W; ++c) big = max_abs_nan(big, b[g][c]);
+        });
+    }
+    mx = __float_as_uint(big);
     row_reduce<TPR>(ss, mx, red[1]);
     const float rs = p.w_pre ? __frsqrt_rn(ss / (float)p.d + p.eps) : 1.0f;
-    // codes: a row that holds an infinity or a NaN gets codes 0 and the scale NaN
-    const bool finite = mx < 0x7f800000u;
-    const float s = finite ? __fdiv_rn(__uint_as_float(mx), 127.0f) : 0.0f;
-    const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    if (p.xq && tid == 0) p.sx[row] = finite ? __fmul_rn(s, rs) : __int_as_float(0x7fc00000);
+    if (p.xq) {
+        // a row that holds an infinity or a NaN gets codes 0 and the scale NaN
+        const bool finite = mx < 0x7f800000u;
+        const float s = finite ? __fdiv_rn(__uint_as_float(mx), 127.0f) : 0.0f;
+        if (tid == 0) p.sx[row] = finite ? __fmul_rn(s, rs) : __int_as_float(0x7fc00000);
+        int8_t* dst = p.xq + row * p.ldq;
+        uint32_t q[G][W == 8 ? 2 : 1];
+        if (s > 0.0f) {
+            const float inv = __frcp_rn(s);
+            if constexpr (W == 8) {
+                all([&](int g, int) {
+                    const Pair v[4] = {Pair(b[g][0], b[g][1]), Pair(b[g][2], b[g][3]), Pair(b[g][4], b[g][5]),
+                                       Pair(b[g][6], b[g][7])};
+                    const uint2 two = int8_codes8(v, s, inv);
+                    q[g][0] = two.x, q[g][W == 8 ? 1 : 0] = two.y;
+                });
+            } else {
+                // as in int8_codes8, with one look at how near any of the thread's values is to a half-integer
+                float off = 0.0f;
+                all([&](int g, int) {
+                    uint32_t word = 0;
 #pragma unroll
-    for (int g = 0; g < G; ++g)
-        if (tid + TPR * g < ng) {
-            const int64_t at = (int64_t)(tid + TPR * g) * W;
-            if (p.xq) {
-                int8_t* dst = p.xq + row * p.ldq + at;
-                if constexpr (W == 8) {
-                    const Pair v[4] = {Pair(b[g][0], b[g][1]), Pair(b[g][2], b[g][3]), Pair(b[g][4], b[g][5]), Pair(b[g][6], b[g][7])};
-                    *reinterpret_cast<uint2*>(dst) = s > 0.0f ? int8_codes8(v, s, inv) : make_uint2(0u, 0u);
-                } else {
-                    uint32_t q = 0;
-                    if (s > 0.0f) {
-#pragma unroll
-                        for (int c = 0; c < W; ++c) q |= ((uint32_t)quant_code_fast(b[g][c], s, inv) & 0xffu) << (8 * c);
+                    for (int c = 0; c < W; ++c) {
+                        const float t = __fmul_rn(b[g][c], inv), a = __fadd_rn(t, 12582912.0f);
+                        off = max_abs_nan(off, __fsub_rn(t, __fsub_rn(a, 12582912.0f)));
+                        word |= (__float_as_uint(a) & 0xffu) << (8 * c);
                     }
-                    if constexpr (W == 4)
-                        *reinterpret_cast<uint32_t*>(dst) = q;
-                    else if constexpr (W == 2)
-                        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)q;
-                    else
-                        *dst = (int8_t)q;
-                }
-            }
-            if (p.n_out) {
+                    q[g][0] = word;
+                });
+                if (!(off < 0.49997f))
+                    all([&](int g, int) {
+                        uint32_t word = 0;
 #pragma unroll
-                for (int c = 0; c < W; ++c) r[g][c] *= rs;
-                store_vals<W>(p.n_out, row * p.ldn + at, out_dtype, r[g]);
+                        for (int c = 0; c < W; ++c) word |= ((uint32_t)quant_code(b[g][c], s) & 0xffu) << (8 * c);
+                        q[g][0] = word;
+                    });
             }
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g) q[g][0] = q[g][W == 8 ? 1 : 0] = 0u;
         }
+        each([&](int g, int at) {
+            if constexpr (W == 8)
+                *reinterpret_cast<uint2*>(dst + at) = make_uint2(q[g][0], q[g][W == 8 ? 1 : 0]);
+            else if constexpr (W == 4)
+                *reinterpret_cast<uint32_t*>(dst + at) = q[g][0];
+            else if constexpr (W == 2)
+                *reinterpret_cast<uint16_t*>(dst + at) = (uint16_t)q[g][0];
+            else
+                dst[at] = (int8_t)q[g][0];
+        });
+    }
+    if (p.n_out)
+        each([&](int g, int at) {
+#pragma unroll
+            for (int c = 0; c < W; ++c) r[g][c] *= rs;
+            store_vals<W>(p.n_out, row * p.ldn + at, out_dtype, r[g]);
+        });
 }
 
 // 8 values of a row as they are stored.
@@ -401,10 +442,6 @@ __device__ __forceinline__ void load_weights(const float* p, int at, float offse
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = w[i] + Pair(offset, offset);
     }
-}
-
-__device__ __forceinline__ float gate_value(const NormParams& p, float g) {
-    return p.gate_sigmoid ? 1.0f / (1.0f + expf(-g)) : g;
 }
 
 // Many rows on 16-byte boundaries, stream and branch of one type.  TPR threads
