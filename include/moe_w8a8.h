@@ -671,8 +671,9 @@ size_t moe_w8a8_linear_workspace_size(const moe_w8a8_linear* l, int32_t max_toke
  *      lies between the rows and after the last one is left as it was
  *   workspace  device, >= moe_w8a8_linear_workspace_size(l, T), 256-byte aligned
  * x and y need the alignment of their type only; rows on 16-byte boundaries
- * are read and written with wider accesses.  Calls that share a workspace must
- * not overlap on the device.  The handle's device must be current.
+ * are read and written with wider accesses.  x, y and the workspace must not
+ * overlap; calls that share a workspace must not overlap on the device.  The
+ * handle's device must be current.
  */
 moe_status moe_w8a8_linear_forward(const moe_w8a8_linear* l, const void* x, int64_t ldx, int32_t T, void* y, int64_t ldy,
                                    void* workspace, size_t workspace_bytes, moe_stream_t stream);

@@ -240,3 +240,49 @@ def test_refusals_of_live_handles(M):
         M.moe_w8a8_sample(z(4, 50, dt=torch.float32), sx, z(4, dt=torch.int32), allowed=z(4, 1, dt=torch.int32))
     # an empty batch is no call
     M.moe_w8a8_sample(z(0, 50, dt=torch.float32), z(0, dt=torch.float32), z(0, dt=torch.int32))
+
+
+def test_offsets_past_32_bits(M):
+    """Rows so far apart that an element's offset passes 32 bits give what neighbouring rows give."""
+    T, k, n, V, far = 3, 320, 200, 3000, (1 << 30) + 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    lin = M.moe_w8a8_linear_prepare_codes(M.make_linear_config(n, k),
+                                          torch.randint(-127, 128, (n, k), generator=g, device="cuda", dtype=torch.int8),
+                                          torch.rand(n, generator=g, device="cuda"))
+    wide = torch.empty(T * far, dtype=torch.bfloat16, device="cuda")
+    at = lambda cols, off=0: wide.as_strided((T, cols), (far, 1), off)  # noqa: E731
+    x = torch.randn(T, k, generator=g, device="cuda").bfloat16()
+    ws = torch.empty(M.moe_w8a8_linear_workspace_size(lin, 400), dtype=torch.uint8, device="cuda")
+    y = torch.empty(T, n, dtype=torch.bfloat16, device="cuda")
+    M.moe_w8a8_linear_forward(lin, x, T, y, ws)
+    at(k).copy_(x)
+    M.moe_w8a8_linear_forward(lin, at(k), T, at(n, 1024), ws)
+    assert torch.equal(at(n, 1024), y)
+    # codes that far apart, through the tensor maps
+    codes = torch.empty(T * far, dtype=torch.int8, device="cuda").as_strided((T, k), (far, 1))
+    sx = torch.empty(T, device="cuda")
+    cfg = M.make_norm_config(k)
+    near = torch.empty(T, k, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    w = torch.rand(k, generator=g, device="cuda") + 0.5
+    nn = torch.empty(T, k, dtype=torch.bfloat16, device="cuda")
+    M.moe_w8a8_block_norm(cfg, T, b=x, x=x, w_pre=w, n_out=nn, xq=near[0], sx=near[1])
+    M.moe_w8a8_block_norm(cfg, T, b=at(k), x=at(k), w_pre=w, n_out=at(k, 4096), xq=codes, sx=sx)
+    assert torch.equal(at(k, 4096), nn) and torch.equal(codes, near[0]) and torch.equal(sx, near[1])
+    M.moe_w8a8_linear_forward_codes(lin, near[0], near[1], T, y)
+    M.moe_w8a8_linear_forward_codes(lin, codes, sx, T, at(n, 8192))
+    assert torch.equal(at(n, 8192), y)
+    # rows off every boundary, and the logits
+    odd = wide.as_strided((T, k), (far - 1, 1), 1)
+    odd.copy_(x)
+    n_odd, n_near = torch.empty_like(nn), torch.empty(T, k + 1, dtype=torch.bfloat16, device="cuda")[:, 1:]
+    M.moe_w8a8_block_norm(cfg, T, b=odd, x=odd, w_pre=w, n_out=n_odd)
+    M.moe_w8a8_block_norm(cfg, T, b=x, x=x, w_pre=w, n_out=n_near)      # the same accesses, rows next to each other
+    assert torch.equal(n_odd, n_near)
+    logits = torch.randn(T, V, generator=g, device="cuda").bfloat16()
+    at(V, 16384).copy_(logits)
+    u, p = torch.rand(T, generator=g, device="cuda"), torch.full((T,), 0.7, device="cuda")
+    tok = torch.empty(2, T, dtype=torch.int32, device="cuda")
+    M.moe_w8a8_sample(logits, u, tok[0], top_p=p)
+    M.moe_w8a8_sample(at(V, 16384), u, tok[1], top_p=p)
+    assert torch.equal(tok[0], tok[1])
