@@ -780,8 +780,8 @@ typedef struct {
     const int32_t* allowed;    /* [rows][ceil(vocab / 32)] words, bit i of word j: token 32 j + i;
                                   rows ld_allowed words apart.  NULL: every token                */
     int64_t ld_allowed;
-    const float* temperature;  /* [rows]; not above 1e-36: the largest logit (lowest index),
-                                  prob 1.  NULL: 1                                               */
+    const float* temperature;  /* [rows]; not above 1e-36, or NaN: the largest logit (lowest index),
+                                  prob 1; above 3e38 counts as 3e38.  NULL: 1                    */
     const int32_t* top_k;      /* [rows]; not above 0: off.  NULL: off                           */
     const float* top_p;        /* [rows]; not below 1: off.  NULL: off                           */
     const float* min_p;        /* [rows]; not above 0: off, above 1 counts as 1.  NULL: off       */

@@ -139,6 +139,18 @@ def test_values_at_the_ends(M):
     check(M, dev(x), one * f(1 - 2.0 ** -24))
 
 
+def test_temperatures_that_are_no_numbers(M):
+    """A NaN is not above the smallest temperature: greedy.  Infinity counts as 3e38."""
+    rng = np.random.default_rng(23)
+    for V in (1, 700, 40000):
+        x = rng.standard_normal((6, V)).astype(np.float32) * 4
+        u = rng.random(6).astype(np.float32)
+        t = np.array([np.nan, 1.0, np.nan, np.inf, 3.4e38, -np.inf], np.float32)
+        check(M, dev(x), u, temperature=t)
+        check(M, dev(x), u, temperature=t, top_k=np.full(6, 5, np.int32), top_p=np.full(6, 0.5, np.float32))
+        check(M, dev(x), u, temperature=t, min_p=np.full(6, 0.5, np.float32))
+
+
 def test_many_rows_and_flat_masses(M):
     rng = np.random.default_rng(11)
     x = rng.standard_normal((300, 5000)).astype(np.float32) * 0.5

@@ -950,7 +950,8 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
         }
         if (r.tid < (-r.n & 3)) r.logits[r.n + r.tid] = minus_inf();
     }
-    const float temp = p.temperature ? fminf(p.temperature[row], 3e38f) : 1.0f;
+    const float given = p.temperature ? p.temperature[row] : 1.0f;
+    const float temp = given > 3e38f ? 3e38f : given;   // (a NaN stays one: greedy)
     const int top_k = p.top_k ? p.top_k[row] : 0;
     const float top_p = p.top_p && p.top_p[row] < 1.0f ? p.top_p[row] : 1.0f;   // (a NaN is off)
     const float min_p = p.min_p ? p.min_p[row] : 0.0f;
