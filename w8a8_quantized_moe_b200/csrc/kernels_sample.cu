@@ -148,6 +148,13 @@ struct Softmax {
     __device__ __forceinline__ double exact(float l) const { return exp2(((double)l - m) * cd); }
 };
 
+// The two halves of a cluster barrier: a block's shared memory may be accessed from
+// another one only when it is known to have started.  (Not .aligned: a warp's lanes
+// need not have come back together.)  Announcing the start orders nothing before it.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 __device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -219,10 +226,14 @@ struct Row {
         turn ^= 1;
         return total;
     }
+    // The largest of v over the cluster: its first exchange.  Every thread has arrived
+    // at the cluster's barrier when its block started; waiting here, after the row has
+    // been read, costs nothing.
     __device__ float max_logit(float v) {
         uint32_t k = __reduce_max_sync(0xffffffffu, key_of(v));
         if (lane == 0) sh->warp_sum[warp] = k;
         __syncthreads();
+        cluster_wait();
         if (warp == 0) {
             k = __reduce_max_sync(0xffffffffu, lane < kSaWarps ? (uint32_t)sh->warp_sum[lane] : 0u);
             if (lane < nb) *cl.map_shared_rank(&sh->slots[turn][rank], lane) = k;
@@ -254,8 +265,8 @@ struct Row {
     // A block's last step: the others leave, the first one when none of them
     // reads its shared memory any more.
     __device__ void leave() {
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        if (rank == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        cluster_arrive();
+        if (rank == 0) cluster_wait();
     }
 };
 
@@ -904,6 +915,7 @@ __global__ void __launch_bounds__(kSaThreads, 2) sample_kernel(const SampleParam
     if (r.tid < 32) shared.tab[r.tid] = (uint32_t)rint(exp2(30.0 + r.tid / 32.0));
     if (r.tid < 2) shared.list_count[r.tid] = 0;
     for (int i = r.tid; i < kHistWords; i += kSaThreads) r.hist[i] = 0;
+    cluster_started();   // this block has started; waited for before the first exchange (max_logit)
     pdl_wait();
 
     // the row's logits into shared memory
