@@ -72,3 +72,19 @@ def test_other_blocks_memory_after_a_cluster_barrier(name):
             "cluster_started" in before and "cluster_wait" in before[before.index("cluster_started"):])
         assert whole, (kernel, order[:first + 1])
     assert seen > 0
+
+
+@pytest.mark.parametrize("name", ["kernels_linear.cu", "kernels_tc.cu"])
+def test_dependents_start_after_tensor_memory_is_held(name):
+    """A block lets the next kernel start only when it holds its tensor memory (a barrier lies between): blocks of the
+    next kernel that took what it waits for would not give it back before it ends."""
+    kernels, functions = load(name)
+    seen = 0
+    for kernel, body in kernels.items():
+        order = steps(body, functions, ("tcgen05.alloc", "pdl_trigger", "__syncthreads", "cluster_sync_all"))
+        if "tcgen05.alloc" not in order or "pdl_trigger" not in order:
+            continue
+        seen += 1
+        between = order[order.index("tcgen05.alloc"):order.index("pdl_trigger")]
+        assert "__syncthreads" in between or "cluster_sync_all" in between, (kernel, order)
+    assert seen > 0

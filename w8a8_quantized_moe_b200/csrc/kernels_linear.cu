@@ -283,10 +283,12 @@ __global__ void __launch_bounds__(kSmallThreads) linear_small_kernel(const __gri
                      "r"(kCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    pdl_trigger();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // only now: the next kernel's blocks must not hold tensor memory that this block
+    // still asks for, since they wait for this kernel to end before they free it
+    pdl_trigger();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort = &ctl->abort;
 
