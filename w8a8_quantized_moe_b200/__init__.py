@@ -700,11 +700,12 @@ def _device() -> int:
 
 
 class Linear:
-    """Owner of a prepared dense product (destroyed with the object)."""
+    """Owner of a prepared dense product (destroyed with the object).  `cfg` is
+    a copy: the caller's may serve for the next product."""
 
     def __init__(self, handle: ctypes.c_void_p, cfg: moe_w8a8_linear_config, smooth: bool):
         self.handle = handle
-        self.cfg = cfg
+        self.cfg = moe_w8a8_linear_config.from_buffer_copy(cfg)
         self.smooth = smooth
         self.n, self.k = cfg.n, cfg.k
         self.x_dtype, self.y_dtype = _act_dtype(cfg.in_dtype), _act_dtype(cfg.out_dtype)
@@ -766,10 +767,10 @@ def moe_w8a8_linear_forward_codes(l: Linear, xq, sx, T: int, y, stream=None):
 
 def moe_w8a8_linear_export(l: Linear, stream=None) -> dict:
     torch = _torch()
-    c, dev = l.cfg, torch.device("cuda", _device())
-    out = dict(wq=torch.empty((c.n, c.k), dtype=torch.int8, device=dev),
-               sw=torch.empty(c.n, dtype=torch.float32, device=dev),
-               inv_s=torch.empty(c.k, dtype=torch.float32, device=dev) if l.smooth else None)
+    dev = torch.device("cuda", _device())
+    out = dict(wq=torch.empty((l.n, l.k), dtype=torch.int8, device=dev),
+               sw=torch.empty(l.n, dtype=torch.float32, device=dev),
+               inv_s=torch.empty(l.k, dtype=torch.float32, device=dev) if l.smooth else None)
     _check(lib().moe_w8a8_linear_export(l.handle, out["wq"].data_ptr(), out["sw"].data_ptr(),
                                         out["inv_s"].data_ptr() if l.smooth else None, _stream(stream)),
            "moe_w8a8_linear_export")
