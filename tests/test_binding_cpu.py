@@ -26,3 +26,14 @@ def test_a_product_keeps_its_own_configuration(M, monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda size, dtype, device: asked.append(size) or empty(size, dtype=dtype))
     M.moe_w8a8_linear_export(lin)
     assert asked == [(48, 32), 48, 32]
+
+
+def test_a_layer_keeps_its_own_configuration(M):
+    """The sizes that a layer's calls check their tensors by are those that it was prepared with."""
+    import torch
+    cfg = M.make_config(256, 512, 8, 2, in_dtype=M.MOE_F32, out_dtype=M.MOE_F32)
+    w = M.Weights(None, cfg)
+    cfg.d, cfg.n_experts = 128, 4
+    assert (w.cfg.d, w.cfg.n_experts, w.n_local) == (256, 8, 8)
+    with pytest.raises(ValueError, match="x holds"):
+        M.moe_w8a8_forward(w, torch.zeros(16 * 128), 16, None, None, torch.zeros(16 * 256), torch.zeros(16))

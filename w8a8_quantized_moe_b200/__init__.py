@@ -302,12 +302,13 @@ def moe_w8a8_calibrate_absmax(x, absmax, stream=None):
 
 class Weights:
     """Owner of a prepared-weights handle (destroyed with the object); it
-    holds experts [expert_first, expert_first + n_local) of the layer."""
+    holds experts [expert_first, expert_first + n_local) of the layer.  `cfg`
+    is a copy: the caller's may serve for the next layer."""
 
     def __init__(self, handle: ctypes.c_void_p, cfg: moe_w8a8_config, expert_first: int = 0,
                  n_local: int | None = None):
         self.handle = handle
-        self.cfg = cfg
+        self.cfg = cfg = moe_w8a8_config.from_buffer_copy(cfg)
         self.expert_first = expert_first
         self.n_local = cfg.n_experts if n_local is None else n_local
 
