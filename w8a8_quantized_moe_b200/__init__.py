@@ -8,6 +8,7 @@ there is no fallback, and importing a missing library fails loudly.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -276,6 +277,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made_on(stream):
+    """Tensors made inside belong to the stream that a call was given: the
+    allocator then hands out no block that work on another stream still uses."""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _torch().cuda
+    return cuda.stream(cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _check(status: int, where: str):
     if status != MOE_OK:
         raise MoeError(status, where)
@@ -419,13 +429,14 @@ def moe_w8a8_export_weights(w: Weights, stream=None) -> dict:
     c = w.cfg
     E, d, f = w.n_local, c.d, c.f
     dev = torch.device("cuda")
-    out = dict(wq_gate=torch.empty((E, f, d), dtype=torch.int8, device=dev),
-               wq_up=torch.empty((E, f, d), dtype=torch.int8, device=dev),
-               sw_gate=torch.empty((E, f), dtype=torch.float32, device=dev),
-               sw_up=torch.empty((E, f), dtype=torch.float32, device=dev),
-               wq_down=torch.empty((E, d, f), dtype=torch.int8, device=dev),
-               sw_down=torch.empty((E, d), dtype=torch.float32, device=dev),
-               inv_s=torch.empty((d,), dtype=torch.float32, device=dev))
+    with _made_on(stream):
+        out = dict(wq_gate=torch.empty((E, f, d), dtype=torch.int8, device=dev),
+                   wq_up=torch.empty((E, f, d), dtype=torch.int8, device=dev),
+                   sw_gate=torch.empty((E, f), dtype=torch.float32, device=dev),
+                   sw_up=torch.empty((E, f), dtype=torch.float32, device=dev),
+                   wq_down=torch.empty((E, d, f), dtype=torch.int8, device=dev),
+                   sw_down=torch.empty((E, d), dtype=torch.float32, device=dev),
+                   inv_s=torch.empty((d,), dtype=torch.float32, device=dev))
     _check(lib().moe_w8a8_export_weights(w.handle, *(ctypes.c_void_p(out[k].data_ptr()) for k in
                                                      ("wq_gate", "wq_up", "sw_gate", "sw_up",
                                                       "wq_down", "sw_down", "inv_s")),
@@ -769,9 +780,10 @@ def moe_w8a8_linear_forward_codes(l: Linear, xq, sx, T: int, y, stream=None):
 def moe_w8a8_linear_export(l: Linear, stream=None) -> dict:
     torch = _torch()
     dev = torch.device("cuda", _device())
-    out = dict(wq=torch.empty((l.n, l.k), dtype=torch.int8, device=dev),
-               sw=torch.empty(l.n, dtype=torch.float32, device=dev),
-               inv_s=torch.empty(l.k, dtype=torch.float32, device=dev) if l.smooth else None)
+    with _made_on(stream):
+        out = dict(wq=torch.empty((l.n, l.k), dtype=torch.int8, device=dev),
+                   sw=torch.empty(l.n, dtype=torch.float32, device=dev),
+                   inv_s=torch.empty(l.k, dtype=torch.float32, device=dev) if l.smooth else None)
     _check(lib().moe_w8a8_linear_export(l.handle, out["wq"].data_ptr(), out["sw"].data_ptr(),
                                         out["inv_s"].data_ptr() if l.smooth else None, _stream(stream)),
            "moe_w8a8_linear_export")
