@@ -37,3 +37,14 @@ def test_a_layer_keeps_its_own_configuration(M):
     assert (w.cfg.d, w.cfg.n_experts, w.n_local) == (256, 8, 8)
     with pytest.raises(ValueError, match="x holds"):
         M.moe_w8a8_forward(w, torch.zeros(16 * 128), 16, None, None, torch.zeros(16 * 256), torch.zeros(16))
+
+
+def test_the_stride_of_a_single_row_is_not_used(M):
+    """One row of a wider buffer is taken like a row alone, whatever the buffer's stride: codes with a stride that is no
+    multiple of 16 are not refused, activations off the 16-byte boundaries keep the wide accesses."""
+    import torch
+    for buffer in (torch.zeros(8, 300, dtype=torch.int8), torch.zeros(8, 201, dtype=torch.int8), torch.zeros(1, 200, dtype=torch.int8)):
+        assert M._matrix(buffer[:, :200], 1, 200, "xq", torch.int8, -1) == (buffer.data_ptr(), 208)
+        assert M._matrix(buffer, 1, 200, "xq", torch.int8, -1) == (buffer.data_ptr(), 208)
+    two = torch.zeros(8, 300, dtype=torch.int8)
+    assert M._matrix(two, 2, 200, "xq", torch.int8, -1) == (two.data_ptr(), 300)

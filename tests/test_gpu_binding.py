@@ -56,3 +56,31 @@ def test_export_after_the_configuration_changed(M):
         made.append((M.moe_w8a8_linear_prepare_codes(cfg, wq, torch.rand(n, device="cuda")), wq))
     for lin, wq in made:
         assert torch.equal(M.moe_w8a8_linear_export(lin)["wq"], wq)
+
+
+def test_one_row_of_a_wider_buffer(M):
+    """A single token's codes, activations, output and logits as a row of a buffer of any stride."""
+    lin, wq = product(M, 70, 200)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    codes = torch.randint(-127, 128, (8, 300), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(1, generator=g, device="cuda")
+    y = [torch.full((4, n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (70, 77)]
+    M.moe_w8a8_linear_forward_codes(lin, codes[:1, :200].contiguous(), sx, 1, y[0])
+    M.moe_w8a8_linear_forward_codes(lin, codes[:1, :200], sx, 1, y[1])
+    assert torch.equal(y[0][0], y[1][0, :70]) and (y[1][0, 70:] == 7).all() and (y[1][1:] == 7).all()
+    x = torch.randn(8, 203, generator=g, device="cuda").bfloat16()
+    ws = torch.empty(M.moe_w8a8_linear_workspace_size(lin, 1), dtype=torch.uint8, device="cuda")
+    M.moe_w8a8_linear_forward(lin, x[:1, :200].contiguous(), 1, y[0], ws)
+    M.moe_w8a8_linear_forward(lin, x[:1, :200], 1, y[1], ws)
+    assert torch.equal(y[0][0], y[1][0, :70])
+    q = [torch.empty(1, 208, dtype=torch.int8, device="cuda"), torch.full((2, 300), 9, dtype=torch.int8, device="cuda")]
+    s = [torch.empty(1, device="cuda"), torch.empty(1, device="cuda")]
+    for i in range(2):
+        M.moe_w8a8_block_norm(M.make_norm_config(200), 1, x=x[:1, :200], w_pre=torch.ones(200, device="cuda"), xq=q[i], sx=s[i])
+    assert torch.equal(q[0][0, :200], q[1][0, :200]) and (q[1][0, 200:] == 9).all() and (q[1][1] == 9).all()
+    assert torch.equal(s[0], s[1])
+    u, token = torch.rand(1, generator=g, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    M.moe_w8a8_sample(x[:1, :200].contiguous(), u, token[:1])
+    M.moe_w8a8_sample(x[:1, :200], u, token[1:])
+    assert token[0] == token[1]

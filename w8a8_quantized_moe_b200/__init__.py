@@ -685,7 +685,7 @@ def _matrix(t, rows, cols, name, dtype, dev):
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
     if rows <= 1:
-        ld = max(ld, cols + -cols % 16)   # the stride of a single row is not used; a round one keeps wide accesses
+        ld = cols + -cols % 16   # the stride of a single row is not used; a round one keeps wide accesses
     elif ld < cols:
         raise ValueError(f"{name} has rows {ld} apart that hold {cols} values")
     return t.data_ptr(), ld
