@@ -708,7 +708,9 @@ void moe_w8a8_linear_destroy(moe_w8a8_linear* l);
  * rint(v / s), sx = s / rms(r) (the row's rms cancels in v / s).  Without
  * w_pre the codes are those of r, the layer's own quantisation of a token.
  * The gate g is 1, a value per channel, per token or per element, or its
- * sigmoid.  Sums of squares are held in fp32: |values| up to 1e18.
+ * sigmoid.  Sums of squares are held in fp32, so both norms take |values| up to
+ * 1e17 (1.8e19 / sqrt(d)); past that a row's rms is infinite, and its n and sx
+ * are 0.
  * ------------------------------------------------------------------------ */
 
 enum {

@@ -137,3 +137,15 @@ def test_limits_match_the_header(M):
     for name in ("MOE_LINEAR_MAX_N", "MOE_LINEAR_MAX_K", "MOE_NORM_MAX_D", "MOE_SAMPLE_MAX_VOCAB", "MOE_SAMPLE_MAX_ROWS"):
         value = re.search(rf"#define {name} (.+)", text).group(1)
         assert eval(value) == getattr(M, name), name
+
+
+def test_the_norms_range_fits_fp32():
+    """The largest values that the header allows leave the sum of squares of the longest row within fp32."""
+    import os
+    import re
+    import numpy as np
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "moe_w8a8.h")).read()
+    part = re.sub(r"\s*\n \*\s*", " ", text[text.index("The norms around a block"):])
+    bound = float(re.search(r"\|values\| up to (\d+e\d+)", part).group(1))
+    longest = int(re.search(r"#define MOE_NORM_MAX_D (\d+)", text).group(1))
+    assert longest * bound ** 2 < float(np.finfo(np.float32).max)

@@ -1,0 +1,58 @@
+"""The norms around a block at the ends of their ranges: the largest values, long rows in large batches, rows of zeros
+and rows that hold an infinity or a NaN, in the kernel for few rows and in the one for many."""
+import numpy as np
+import pytest
+import torch
+
+from tests import around_ref as R
+from tests.test_gpu_block_norm import DT, RMS_U, U32, UBF, host
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def M():
+    import w8a8_quantized_moe_b200 as mod
+    torch.cuda.set_device(0)
+    return mod
+
+
+@pytest.mark.parametrize("T", [3, 250])
+@pytest.mark.parametrize("d", [16384, 16383, 4096])
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("post", [False, True])
+def test_the_largest_values(M, T, d, typ, post):
+    """Rows whose values are all of the largest size that the norms take, of either sign."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + d)
+    code = M.MOE_F32 if typ == "f32" else M.MOE_BF16
+    largest = torch.tensor(1e17).to(DT[typ])
+    if largest.double() > 1e17:
+        largest = torch.nextafter(largest, torch.zeros_like(largest))
+    sign = lambda: torch.randint(0, 2, (T, d), generator=g, device="cuda") * 2.0 - 1  # noqa: E731
+    x = (sign() * largest.cuda()).to(DT[typ])
+    b = (sign() * largest.cuda()).to(DT[typ])
+    w_post = torch.rand(d, generator=g, device="cuda") + 0.5
+    w_pre = torch.rand(d, generator=g, device="cuda") + 0.5
+    x_out, n_out = torch.empty_like(x), torch.empty(T, d, device="cuda")
+    xq, sx = torch.empty(T, 16384, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    # r = x / 2 + 10 norm(b), or x / 2 + b / 2: within the range too
+    cfg = M.make_norm_config(d, code, code, M.MOE_F32, residual_scale=0.5, branch_scale=10.0 if post else 0.5)
+    M.moe_w8a8_block_norm(cfg, T, b=b, x=x, w_post=w_post if post else None, w_pre=w_pre, x_out=x_out, n_out=n_out, xq=xq, sx=sx)
+    eps = np.float64(np.float32(1e-6))
+    p = host(b) / R.rms(host(b), eps) * host(w_post) * 10 if post else 0.5 * host(b)
+    r = 0.5 * host(x) + p
+    got = host(x_out)
+    tol = 1.01 * 32 * U32 * (0.5 * np.abs(host(x)) + np.abs(p)) + 1.01 * (UBF if typ == "bf16" else U32) * np.abs(r)
+    assert (np.abs(got - r) <= tol).all()
+    inv = 1.0 / R.rms(got, eps)
+    n = got * inv * host(w_pre)
+    assert (np.abs(host(n_out) - n) <= 1.01 * (RMS_U + 4 * U32) * np.abs(n)).all() and (n != 0).any()
+    q, s = R.quantize_rows(got.astype(np.float32) * host(w_pre).astype(np.float32))
+    assert np.array_equal(xq[:, :d].cpu().numpy(), q)
+    want = s.astype(np.float64) * inv[:, 0]
+    assert (want > 0).all() and (np.abs(host(sx) - want) <= 1.01 * (RMS_U + U32) * want).all()
+    if post:   # the norm after the block alone: its values are of order one, the input's of order 1e17
+        M.moe_w8a8_block_norm(M.make_norm_config(d, code, code, M.MOE_F32), T, b=b, w_post=w_post, x_out=x_out)
+        p = host(b) / R.rms(host(b), eps) * host(w_post)
+        assert (np.abs(host(x_out) - p) <= 1.01 * (RMS_U + 3 * U32 + (UBF if typ == "bf16" else U32)) * np.abs(p)).all()
