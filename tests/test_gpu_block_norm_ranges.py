@@ -56,3 +56,30 @@ def test_the_largest_values(M, T, d, typ, post):
         M.moe_w8a8_block_norm(M.make_norm_config(d, code, code, M.MOE_F32), T, b=b, w_post=w_post, x_out=x_out)
         p = host(b) / R.rms(host(b), eps) * host(w_post)
         assert (np.abs(host(x_out) - p) <= 1.01 * (RMS_U + 3 * U32 + (UBF if typ == "bf16" else U32)) * np.abs(p)).all()
+
+
+@pytest.mark.parametrize("T", [3, 250])
+@pytest.mark.parametrize("d", [520, 516, 518, 1001, 4104])
+@pytest.mark.parametrize("where", ["channel", "element", "w_post"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_what_stands_at_a_rows_end(M, T, d, where, value):
+    """An infinite gate or weight of the row's last channel reaches that channel and, through the rms, the others as the
+    formulas have it: the stream is as it is elsewhere, n is finite / infinity = 0 there."""
+    b, x = torch.ones(T, d, device="cuda"), torch.full((T, d), 2.0, device="cuda")
+    w = torch.ones(d, device="cuda")
+    special = torch.ones(d, device="cuda")
+    special[-1] = value
+    x_out, n_out = torch.empty_like(x), torch.empty_like(x)
+    xq, sx = torch.full((T, (d + 15) // 16 * 16), 5, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    gate = {"channel": special, "element": special.expand(T, d).contiguous(), "w_post": None}[where]
+    cfg = M.make_norm_config(d, M.MOE_F32, M.MOE_F32, M.MOE_F32, eps=1e-6,
+                             gate=M.MOE_GATE_NONE if gate is None else getattr(M, "MOE_GATE_" + where.upper()))
+    M.moe_w8a8_block_norm(cfg, T, b=b, x=x, gate=gate, w_post=special if gate is None else w, w_pre=w, x_out=x_out, n_out=n_out,
+                          xq=xq, sx=sx)
+    # 2 + 1 / sqrt(1 + 1e-6); the sum's, root's and products' roundings
+    assert ((x_out[:, :-1].double() - (2 + 1 / np.sqrt(1 + 1e-6))).abs() <= 3 * 20 * U32).all()
+    if np.isinf(value):
+        assert torch.isinf(x_out[:, -1]).all() and (n_out[:, :-1] == 0).all() and torch.isnan(n_out[:, -1]).all()
+    else:
+        assert torch.isnan(x_out[:, -1]).all() and torch.isnan(n_out).all()
+    assert torch.isnan(sx).all() and (xq[:, :d] == 0).all()

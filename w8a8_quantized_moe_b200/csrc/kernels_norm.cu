@@ -301,6 +301,15 @@ __global__ void __launch_bounds__(TPR == 32 ? 256 : TPR, TPR == 32 ? 4 : W == 1 
 #pragma unroll
             for (int c = 0; c < W; ++c) ss = fmaf(r[g][c], r[g][c], ss);
         });
+        // past the row's end an infinite weight or gate of its last values has made 0 a NaN, which is not
+        // the row's (rare, so asked once: zeros kept there by a pass of their own cost 3 to 5%)
+        if (isnan(ss)) {
+            ss = 0.0f;
+            each([&](int g, int) {
+#pragma unroll
+                for (int c = 0; c < W; ++c) ss = fmaf(r[g][c], r[g][c], ss);
+            });
+        }
         times(r, p.w_pre, p.weight_offset);
     }
     if (p.xq) {
