@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from tests import around_ref as R
-from tests.test_gpu_block_norm import DT, RMS_U, U32, UBF, host
+from tests.test_gpu_block_norm import DT, RMS_U, U32, UBF, host, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,60 @@ def test_what_stands_at_a_rows_end(M, T, d, where, value):
     else:
         assert torch.isnan(x_out[:, -1]).all() and torch.isnan(n_out).all()
     assert torch.isnan(sx).all() and (xq[:, :d] == 0).all()
+
+
+@pytest.mark.parametrize("T", [199, 200, 300])
+@pytest.mark.parametrize("d", [4104, 8192, 8200, 16384])
+def test_long_rows_in_large_batches(M, T, d):
+    """The widest blocks of the kernel for many rows, with and without codes, w_post and a gate, in both types."""
+    run_case(M, T, d, "bf16", "bf16", "bf16", False, "none", False, False, False)
+    run_case(M, T, d, "bf16", "bf16", "bf16", True, "channel", False, True, True, offset=1.0, inplace=True)
+    run_case(M, T, d, "f32", "f32", "f32", True, "element", True, True, False, pad=8)
+    run_case(M, T, d, "f32", "f32", "bf16", False, "token", False, True, True)
+
+
+@pytest.mark.parametrize("T", [7, 250])
+@pytest.mark.parametrize("d", [512, 4096, 8192, 16384, 516, 1001])
+@pytest.mark.parametrize("typ", ["f32", "bf16"])
+@pytest.mark.parametrize("branch", [False, True])
+def test_rows_of_zeros_infinities_and_nan(M, T, d, typ, branch):
+    """Zero rows give zeros; a row that holds an infinity or a NaN, in the stream or in the branch, gets codes 0 and the
+    scale NaN, and its neighbours are as without it."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T + d)
+    code = M.MOE_F32 if typ == "f32" else M.MOE_BF16
+    x = torch.randn(T, d, generator=g, device="cuda").to(DT[typ])
+    b = torch.randn(T, d, generator=g, device="cuda").to(DT[typ])
+    w, w_post = (torch.rand(d, generator=g, device="cuda") + 0.5 for _ in range(2))
+    cfg = M.make_norm_config(d, code, code, M.MOE_F32)
+
+    def call():
+        x_out, n_out = torch.empty_like(x), torch.empty(T, d, device="cuda")
+        xq, sx = torch.full((T, 16384), 5, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+        M.moe_w8a8_block_norm(cfg, T, b=b if branch else None, x=x, w_post=w_post if branch else None, w_pre=w, x_out=x_out,
+                              n_out=n_out, xq=xq, sx=sx)
+        return x_out, n_out, xq[:, :d], sx
+
+    clean = call()
+    x[1], b[1] = 0.0, 0.0
+    special = {2: float("inf"), 3: float("nan"), 4: -float("inf")}
+    for t, v in special.items():
+        x[t, (t * 97) % d] = v
+    if branch:
+        b[5, d - 1] = float("nan")
+        b[6, 0] = float("inf")
+        special.update({5: 0.0, 6: 0.0})
+    x_out, n_out, xq, sx = call()
+    for t in range(T):
+        if t == 1:
+            assert (x_out[t] == 0).all() and (n_out[t] == 0).all() and (xq[t] == 0).all() and sx[t] == 0
+        elif t in special:
+            assert (xq[t] == 0).all() and torch.isnan(sx[t])
+        else:
+            assert all(torch.equal(a[t], c[t]) for a, c in zip((x_out, n_out, xq, sx), clean))
+    # n of a row with an infinity: finite / infinity = 0, infinity / infinity is no number; a NaN takes the whole row
+    at = [(t * 97) % d for t in range(5)]
+    for t in (2, 4):
+        others = torch.arange(d, device="cuda") != at[t]
+        assert torch.isnan(n_out[t, at[t]]) and (n_out[t][others] == 0).all() and torch.isinf(x_out[t, at[t]])
+    assert torch.isnan(n_out[3]).all()
