@@ -443,75 +443,43 @@ __device__ uint32_t make_list(Row& r, const Softmax& sm, float t0, float t1, int
 
 __device__ __forceinline__ int pow2_at_least(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
 
-// Sort n entries (a power of two up to E x kSaThreads), falling: thread t holds
-// entries t, t + kSaThreads, ... of the order.  Bitonic; neighbours of a warp
-// exchange by shuffles, a thread's own entries in registers, the others through
-// `buf` (2 x E x kSaThreads words, used in turn).
-template <int E>
-__device__ void sort_falling(uint64_t (&v)[E], uint64_t* buf, int n, int tid) {
+// Sort n entries (a power of two up to kSaThreads), falling: thread t holds entry
+// t of the order.  Bitonic; neighbours of a warp exchange by shuffles, the others
+// through `buf` (2 x kSaThreads words, used in turn).
+__device__ void sort_falling(uint64_t& v, uint64_t* buf, int n, int tid) {
     int turn = 0;
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step > 0; step >>= 1) {
-            if (E > 1 && step >= kSaThreads) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-#pragma unroll
-                    for (int d = 1; d < E; d <<= 1)
-                        if (step == d * kSaThreads && !(e & d)) {
-                            const bool falling = ((e * kSaThreads + tid) & size) == 0;
-                            const uint64_t x = v[e], y = v[(e | d) & (E - 1)];
-                            if ((x < y) == falling) {
-                                v[e] = y;
-                                v[(e | d) & (E - 1)] = x;
-                            }
-                        }
-                continue;
-            }
-            uint64_t* b = buf + turn * E * kSaThreads;
+            uint64_t* b = buf + turn * kSaThreads;
             if (step >= 32) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) b[e * kSaThreads + tid] = v[e];
+                b[tid] = v;
                 __syncthreads();
                 turn ^= 1;
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int i = e * kSaThreads + tid;
-                const uint64_t x = v[e];
-                const uint64_t y = step >= 32 ? b[i ^ step] : __shfl_xor_sync(0xffffffffu, x, step);
-                const bool larger = ((i & size) == 0) == ((i & step) == 0);   // this place keeps the larger one
-                v[e] = (x > y) == larger ? x : y;
-            }
+            const uint64_t y = step >= 32 ? b[tid ^ step] : __shfl_xor_sync(0xffffffffu, v, step);
+            const bool larger = ((tid & size) == 0) == ((tid & step) == 0);   // this place keeps the larger one
+            v = (v > y) == larger ? v : y;
         }
 }
 
-// Bring n entries (list[0 .. n), in any order) into falling order of the
-// entries, or of the entries with their halves exchanged (rising index), with
-// run[i] the mass up to and with entry i.  By one block; list and run are the two
-// halves of its scratch.
-template <int E, bool BY_INDEX>
+// Bring n entries (list[0 .. n), at most kSaThreads, in any order) into falling
+// order of the entries, or of the entries with their halves exchanged (rising
+// index), with run[i] the mass up to and with entry i.  By one block; list and run
+// are the two halves of its scratch.
+template <bool BY_INDEX>
 __device__ void order_by_sort(Row& r, const Softmax& sm, uint64_t* list, uint64_t* run, int n) {
-    uint64_t v[E], at = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        v[e] = i < n ? list[i] : 0;
-        if (BY_INDEX) v[e] = (v[e] << 32) | (v[e] >> 32);
-    }
+    const int i = r.tid;
+    uint64_t v = i < n ? list[i] : 0;
+    if (BY_INDEX) v = (v << 32) | (v >> 32);
     __syncthreads();   // the list is in registers: its place serves the sort
-    sort_falling<E>(v, run, pow2_at_least(n), r.tid);
+    sort_falling(v, run, pow2_at_least(n), i);
     __syncthreads();
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = e * kSaThreads + r.tid;
-        if (BY_INDEX) v[e] = (v[e] << 32) | (v[e] >> 32);
-        uint64_t total;
-        const uint64_t inc = r.block_scan(i < n ? sm.mass(entry_logit(v[e])) : 0, total);
-        if (i < n) {
-            list[i] = v[e];
-            run[i] = at + inc;
-        }
-        at += total;
+    if (BY_INDEX) v = (v << 32) | (v >> 32);
+    uint64_t total;
+    const uint64_t inc = r.block_scan(i < n ? sm.mass(entry_logit(v)) : 0, total);
+    if (i < n) {
+        list[i] = v;
+        run[i] = inc;
     }
     __syncthreads();
 }
@@ -564,7 +532,7 @@ __device__ __forceinline__ void order_list(Row& r, const Softmax& sm, uint64_t* 
     if (n <= kCounted)
         order_by_count<BY_INDEX>(r, sm, list, run, n);
     else
-        order_by_sort<1, BY_INDEX>(r, sm, list, run, n);
+        order_by_sort<BY_INDEX>(r, sm, list, run, n);
 }
 
 // In a longer list no order is formed.  Among the entries e[0 .. n) that are at
