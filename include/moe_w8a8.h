@@ -772,7 +772,9 @@ moe_status moe_w8a8_block_norm(const moe_w8a8_norm_config* cfg, const moe_w8a8_n
  *      u times the mass that is left.
  * Logits of +infinity share the mass evenly.  Results do not depend on the
  * order of execution; masses are held as integers of 2^-45 of the largest one,
- * one unit at least (below 2^-1000 of the largest: none).
+ * one unit at least (below 2^-1000 of the largest: none), each within 3e-9 of
+ * the true one.  The whole in step 3 holds the part of the tokens far below the
+ * largest (less than 1/64 of its mass together) to 2^-23 of the largest mass.
  * ------------------------------------------------------------------------ */
 
 /* Device pointers. */

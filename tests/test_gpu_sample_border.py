@@ -15,6 +15,30 @@ def M():
     return mod
 
 
+@pytest.mark.parametrize("vocab", [5000, 40001, 262144])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 3.0])
+def test_a_cut_beside_a_far_tail(M, vocab, temperature):
+    """Masses 1 and 0.01 at the head and 0.006 in all other tokens together, far below: whether the second token is kept
+    turns on the tail's sum, which is held to 2^-23 of the largest mass, beside sums within 3e-9 of theirs; top_p and the
+    product with it are rounded to 2^-24 and 2^-53.  So a top_p four fp32 steps (2^-22) or more from the border decides
+    as the definition does."""
+    rng = np.random.default_rng(vocab)
+    t = np.float64(np.float32(temperature))
+    x = (t * (np.log(0.006 / vocab) + 0.2 * rng.standard_normal(vocab))).astype(np.float32)
+    first, second = vocab // 3, vocab - 2
+    x[first], x[second] = 0.0, np.float32(t * np.log(0.01))
+    e = np.exp(x.astype(np.float64) / t)
+    border = np.float32(1.0 / e.sum())                  # the first token alone reaches up to this top_p
+    steps = np.array([-4096, -256, -16, -4, 4, 16, 256, 4096])
+    top_p = (border + steps * 2.0 ** -24).astype(np.float32)
+    assert (np.abs(top_p.astype(np.float64) * e.sum() - 1.0) >= 3.4 * 2.0 ** -24).all() and (1 - top_p > 0.011).all()
+    rows = len(steps)
+    logits = dev(np.tile(x, (rows, 1)))
+    u = np.full(rows, 1 - 2.0 ** -24, np.float32)       # the last token that is kept
+    check(M, logits, u, top_p=top_p, temperature=np.full(rows, temperature, np.float32))
+    check(M, logits, u * 0, top_p=top_p, temperature=np.full(rows, temperature, np.float32))
+
+
 @pytest.mark.parametrize("n", [1, 2, 3, 31, 33, 127, 128, 129, 200, 256, 257, 511, 512, 513, 1000, 2047, 2048, 2049, 3000])
 @pytest.mark.parametrize("vocab", [4000, 50000])
 def test_lists_of_every_length(M, n, vocab):

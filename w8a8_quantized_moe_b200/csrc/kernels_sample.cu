@@ -7,8 +7,16 @@
 // the tokens, the first whose running mass exceeds u times the kept mass.
 //
 // Masses are held as integers in units of 2^-45 of the largest one (one unit at
-// least: u = 0 is the first token that takes part), so sums do not depend on
-// the order of the atomics and every comparison is exact.
+// least: u = 0 is the first token that takes part), each within 3e-9 of the true
+// one, so sums do not depend on the order of the atomics.  Three roundings remain,
+// the same on every run:
+//   - The whole mass that top_p is taken of counts the tokens far below the largest
+//     (less than 1/64 of the largest mass together) by an approximate 2^x, summed in
+//     fp32 per thread: off by less than 2^-23 of the largest mass (Softmax::
+//     approximate).  Whether one of them itself is kept goes by its integer mass.
+//   - A histogram's bin drops what is below one unit once for all its tokens, a list
+//     or a pass once for each token: 2^-32 of the largest mass in all.
+//   - Running sums are compared with top_p of the whole as doubles, 2^-53 of a sum.
 //
 // A row belongs to a cluster of thread blocks that keep it in their shared
 // memory: the logits are read from memory once, the later passes read shared
@@ -138,7 +146,11 @@ struct Softmax {
         if (!(t >= t_max - 46.0f * 32)) return t >= t_max - 32000.0f ? 1 : 0;
         return max(fixed(mantissa(l, t), bin(t)), (uint64_t)1);
     }
-    // the mass as a fraction of the largest, to 2^-21
+    // The mass 2^x as a fraction of the largest, for the tokens far below it.  l - max, c
+    // and their product are rounded to fp32, 3 |x| ln 2 < 2.1 |x| units of 2^-24 of the
+    // mass; ex2.approx adds 4, and a thread's sum over up to 64 tokens 64 more.  Masses are
+    // at most 2^-x0, x0 = 6.5 + log2(vocab), so all of them together are off by at most
+    // vocab 2^-x0 (2.1 x0 + 68) < 1.4 of these units.
     __device__ __forceinline__ float approximate(float l) const {
         float e;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(__fsub_rn(l, max_logit), c)));
