@@ -646,7 +646,9 @@ typedef struct moe_w8a8_linear moe_w8a8_linear; /* opaque, library-owned */
  *               max|W_j|^(1-alpha) is folded into the weights; NULL: no smoothing
  * Synchronises `stream`; the inputs may be freed afterwards.  Allocates the
  * handle's device memory (n k bytes, padded to multiples of 256 channels and
- * 128 inputs, and scales); MOE_ERR_OOM if that fails.
+ * 128 inputs, and scales); MOE_ERR_OOM if that fails.  A channel whose weights
+ * hold an infinity or a NaN gives NaN outputs (smoothed, an infinity makes every
+ * channel's NaN).
  */
 moe_status moe_w8a8_linear_prepare(const moe_w8a8_linear_config* cfg, const float* w, const float* bias,
                                    const float* act_absmax, moe_stream_t stream, moe_w8a8_linear** out);

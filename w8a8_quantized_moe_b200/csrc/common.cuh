@@ -171,6 +171,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// The larger of m and |v|, a NaN if there is one.
+__device__ __forceinline__ float max_abs_nan(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
 __device__ __forceinline__ int warp_sum_i(int v) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

@@ -44,6 +44,8 @@ __global__ void linear_input_absmax_kernel(const float* __restrict__ w, int n, f
 }
 
 // sw[n] = max_j |s_j w[j][n]| / 127 (0 past the last channel), 32 channels per block.
+// A channel that holds a NaN gets that scale, so that its outputs are NaN; an infinite
+// one does so by itself (codes 0 times an infinite scale).
 __global__ void __launch_bounds__(256) linear_scales_kernel(const float* __restrict__ w, const float* __restrict__ smooth,
                                                             int k, int n, float* __restrict__ sw) {
     __shared__ float red[8][32];
@@ -53,13 +55,13 @@ __global__ void __launch_bounds__(256) linear_scales_kernel(const float* __restr
         for (int j = ty; j < k; j += 8) {
             float v = w[(int64_t)j * n + c];
             if (smooth) v = __fmul_rn(smooth[j], v);
-            m = fmaxf(m, fabsf(v));
+            m = max_abs_nan(m, v);
         }
     red[ty][tx] = m;
     __syncthreads();
     if (ty == 0) {
-        for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i][tx]);
-        sw[c] = m > 0.0f ? __fdiv_rn(m, 127.0f) : 0.0f;
+        for (int i = 1; i < 8; ++i) m = max_abs_nan(m, red[i][tx]);
+        sw[c] = m == 0.0f ? 0.0f : __fdiv_rn(m, 127.0f);
     }
 }
 

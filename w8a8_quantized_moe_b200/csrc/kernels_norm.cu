@@ -139,13 +139,6 @@ __device__ __forceinline__ void row_reduce(float& sum, uint32_t& mx, float* red)
     }
 }
 
-// The larger magnitude, a NaN if there is one.
-__device__ __forceinline__ float max_abs_nan(float m, float v) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
-    return r;
-}
-
 // The codes of eight values for scale s > 0 (inv = fp32(1 / s)): identical to
 // quant_code of each.  t = v inv is within 2.3e-5 of the IEEE quotient where that
 // is below 128 (quant_code_fast), so unless t lies within 3e-5 of a half-integer
