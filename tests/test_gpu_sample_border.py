@@ -57,3 +57,35 @@ def test_lists_of_every_length(M, n, vocab):
     check(M, dev(x), u, top_k=rng.integers(1, n + 1, rows).astype(np.int32), top_p=p)
     check(M, dev(x), u, top_p=p)
     check(M, dev(x), u, top_p=p, min_p=rng.uniform(0.05, 0.6, rows).astype(np.float32))
+
+
+def test_settings_that_are_no_numbers(M):
+    """A NaN top_p or min_p is off, a NaN u is 0."""
+    rng = np.random.default_rng(5)
+    f = np.float32
+    for vocab in (300, 30000):
+        x = rng.standard_normal((4, vocab)).astype(f) * 3
+        u = rng.random(4).astype(f)
+        nan = np.full(4, np.nan, f)
+        check(M, dev(x), u, top_p=nan)
+        check(M, dev(x), u, min_p=nan)
+        check(M, dev(x), u, top_k=np.full(4, 20, np.int32), top_p=nan, min_p=nan)
+        tokens = [torch.empty(4, dtype=torch.int32, device="cuda") for _ in range(2)]
+        M.moe_w8a8_sample(dev(x), dev(nan), tokens[0], top_p=dev(np.full(4, 0.8, f)))
+        M.moe_w8a8_sample(dev(x), dev(u * 0), tokens[1], top_p=dev(np.full(4, 0.8, f)))
+        assert torch.equal(*tokens)
+
+
+def test_the_most_rows(M):
+    rows, vocab = M.MOE_SAMPLE_MAX_ROWS, 33
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn(rows, vocab, generator=g, device="cuda")
+    u = torch.rand(rows, generator=g, device="cuda")
+    token = torch.full((rows + 1,), 99, dtype=torch.int32, device="cuda")
+    M.moe_w8a8_sample(x, u, token, temperature=torch.zeros(rows, device="cuda"))
+    assert torch.equal(token[:rows], x.argmax(1).int()) and token[rows] == 99
+    M.moe_w8a8_sample(x, u * 0, token)
+    assert (token[:rows] == 0).all() and token[rows] == 99
+    M.moe_w8a8_sample(x, u, token, top_k=torch.ones(rows, dtype=torch.int32, device="cuda"))
+    assert torch.equal(token[:rows], x.argmax(1).int())
