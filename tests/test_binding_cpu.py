@@ -48,3 +48,18 @@ def test_the_stride_of_a_single_row_is_not_used(M):
         assert M._matrix(buffer, 1, 200, "xq", torch.int8, -1) == (buffer.data_ptr(), 208)
     two = torch.zeros(8, 300, dtype=torch.int8)
     assert M._matrix(two, 2, 200, "xq", torch.int8, -1) == (two.data_ptr(), 300)
+
+
+def test_missing_tensors_are_named(M, monkeypatch):
+    """A tensor that is missing or no tensor is refused by its name, like one of the wrong kind."""
+    import torch
+    monkeypatch.setattr(M, "_device", lambda: -1)       # the host, as the checks see it
+    lin = M.Linear(None, M.make_linear_config(16, 32), False)
+    x, y = torch.zeros(2, 32, dtype=torch.bfloat16), torch.zeros(2, 16, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="workspace"):
+        M.moe_w8a8_linear_forward(lin, x, 2, y, None)
+    with pytest.raises(TypeError, match="x must"):
+        M.moe_w8a8_linear_forward(lin, None, 2, y, None)
+    for logits, error in ((None, TypeError), ([[1.0]], TypeError), (torch.zeros(5), ValueError)):
+        with pytest.raises(error, match="logits"):
+            M.moe_w8a8_sample(logits, torch.zeros(2), torch.zeros(2, dtype=torch.int32))

@@ -762,7 +762,10 @@ def moe_w8a8_linear_forward(l: Linear, x, T: int, y, workspace, stream=None):
     dev = _device()
     xp, ldx = _matrix(x, T, l.k, "x", l.x_dtype, dev)
     yp, ldy = _matrix(y, T, l.n, "y", l.y_dtype, dev)
-    wp = _vector(workspace, 0, "workspace", workspace.dtype, dev)
+    try:
+        wp = _vector(workspace, 0, "workspace", workspace.dtype, dev)
+    except AttributeError:
+        _refuse(workspace, "workspace", None, dev)
     _check(lib().moe_w8a8_linear_forward(l.handle, xp, ldx, T, yp, ldy, wp, _nbytes(workspace), _stream(stream)),
            "moe_w8a8_linear_forward")
 
@@ -839,7 +842,12 @@ def moe_w8a8_sample(logits, u, token, temperature=None, top_k=None, top_p=None, 
                     stream=None):
     torch = _torch()
     dev, f32, i32 = _device(), torch.float32, torch.int32
-    rows, vocab = logits.shape
+    try:
+        rows, vocab = logits.shape
+    except AttributeError:
+        _refuse(logits, "logits", None, dev)
+    except ValueError:
+        raise ValueError(f"logits must be [rows][vocab], got {list(logits.shape)}") from None
     if rows == 0:
         return
     bf16 = logits.dtype == torch.bfloat16
