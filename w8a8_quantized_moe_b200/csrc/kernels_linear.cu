@@ -729,7 +729,8 @@ struct LinearPlan {
 // with 64 in two parts 7.2 (7.4), with 128 11.0 (10.3); 256 x 4096 x 4096 with 64 in
 // two parts 12.1 (12.4), with 128 in four 11.7 (11.6), in two 13.6 (13.8); 1024 x
 // 4096 x 4096 with 128 20.6 (20.9); 32 x 4096 x 6144 with 32 in four parts 7.2
-// (7.9); 4096 x 4096 x 4096 on pairs 63 to 77 (66).
+// (7.9); 4096 x 4096 x 4096 on pairs 56 to 77 (66).  It has no term for memory: 64 x
+// 4096 x 32000 is 18 in it, its bytes alone take 21 and the launch takes 25.
 LinearPlan linear_plan(const LinearTiles& t, int T, bool quantize) {
     LinearPlan best{0, 1};
     const int64_t channels = (t.n + kTile - 1) / kTile;

@@ -452,11 +452,12 @@ __device__ __forceinline__ void load_weights(const float* p, int at, float offse
 // row's fixed work (two reductions, a division) is shared by many values; the row
 // is kept as it is stored (the new stream is rounded to its type anyway), twice
 // unpacked, so that it takes 4 registers per 8 values of bf16.  Measured, 16384 x
-// 4096 bf16, us: residual add and norm 81 (6.6 TB/s), with both norms and a gate
-// 95, codes alone 52 (bound by instructions, 20 per value); blocks that stay and
-// take every n-th row 97, 101 and 56; twice the values per thread 100, 130 and 63
-// (registers); 512 threads per row, the next row's loads early, 88, 144 and 87 (a
-// row's fixed work).
+// 4096 bf16, us: residual add and norm 80 (6.7 TB/s), with both norms and a gate
+// 92, codes alone 51 to 55 (instructions: 20 per value, issue slots 63% used), codes
+// of a norm 60, smoothed 79 (each weight vector is read again for each row); blocks
+// that stay and take every n-th row 97, 101 and 56; twice the values per thread 100,
+// 130 and 63 (registers); 512 threads per row, the next row's loads early, 88, 144
+// and 87 (a row's fixed work).
 // BRANCH, POST, CODES: b, w_post and xq are given.
 template <int TPR, int G, bool BF16, bool BRANCH, bool POST, bool CODES>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) block_norm_rows_kernel(const NormParams p) {
@@ -694,14 +695,23 @@ bool in_groups(const NormParams& p, int W) {
            (p.gate_kind != MOE_GATE_CHANNEL || ok(p.gate, 0, 4));   // (xq is on 16 bytes with its rows)
 }
 
-// Rows from which few threads per row do better (599 x 8192 with many: 16.9 us, 600 with
-// few: 9.3; up to 200 rows both are bound by the call).
+// Rows from which few threads per row take over: one count for every width.  Measured
+// around it, residual add and norm of bf16, us a launch with many threads per row / with
+// few: 200 x 1024 2.4 / 3.3, 200 x 4096 3.3 / 3.8, 200 x 8192 5.9 / 4.9, 200 x 16384 8.3 /
+// 5.9; 600 x 1024 3.3 / 3.6, 600 x 4096 6.8 / 5.3, 600 x 8192 12.7 / 7.8; 64 x 8192 3.5 /
+// 3.6.  (Rows of at most 512 values do better with few threads at any count, 1 x 512 2.3 /
+// 2.1, rows of 1024 with many up to 1200; both by less than a call takes on the host.)
 constexpr int64_t kManyRows = 200;
 
 }  // namespace
 
 cudaError_t launch_block_norm(const NormParams& p, cudaStream_t s) {
     const int d = p.d;
+    // For a few rows, the block whose threads hold the row in one group of 8 each (a warp
+    // up to 512 values, 1024 threads at most).  Half the threads with two groups each: 64 x
+    // 1024 2.6 us instead of 2.2, 64 x 4096 2.9 instead of 2.8, 64 x 8192 3.7 instead of
+    // 3.5 (but 199 x 8192 4.6 instead of 5.9).  Narrower groups: as many threads, more
+    // groups each.
     if (in_groups(p, 8)) {
         if (p.T >= kManyRows && (!p.b || p.in_dtype == p.res_dtype))
             return p.res_dtype == MOE_BF16 ? run_rows_by_size<true>(p, s) : run_rows_by_size<false>(p, s);
