@@ -40,8 +40,9 @@ def test_export_on_another_stream(M, what, as_int):
     got = export(handle, stream=st.cuda_stream if as_int else st)
     torch.cuda.synchronize()
     assert (kept == 5).all()
-    for key, v in want.items():
-        assert (v is None and got[key] is None) or torch.equal(v, got[key])
+    for out in (got, export(handle, stream=0), export(handle, stream=torch.cuda.default_stream())):
+        for key, v in want.items():
+            assert (v is None and out[key] is None) or torch.equal(v, out[key])
 
 
 def test_export_after_the_configuration_changed(M):
